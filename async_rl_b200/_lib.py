@@ -11,7 +11,8 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libbi_islos
 
 EXPORTED = ("bi_workspace_bytes", "bi_workspace_bytes_min", "bi_workspace_bytes_pstore", "bi_logprob_fwd", "bi_logprob_fwd_noalloc", "bi_is_loss_fwd_bwd", "bi_d3_stats",
             "bi_status_string", "bi_version", "bi_debug_force_timeout_once", "bi_profile_enable",
-            "bi_profile_reset", "bi_profile_read", "bi_gemm_bf16", "bi_rmsnorm")
+            "bi_profile_reset", "bi_profile_read", "bi_gemm_bf16", "bi_rmsnorm", "bi_qk_norm_rope",
+            "bi_qk_norm_rope_bwd_workspace_bytes", "bi_qk_norm_rope_bwd", "bi_adamw_step")
 
 STATUS_NAMES = {0: "BI_OK", 1: "BI_ERR_INVALID_ARG", 2: "BI_ERR_UNSUPPORTED_SHAPE", 3: "BI_ERR_WORKSPACE",
                 4: "BI_ERR_CUDA", 5: "BI_ERR_TIMEOUT", 6: "BI_ERR_BAD_TARGET", 7: "BI_ERR_NONFINITE",
@@ -24,6 +25,21 @@ class LossCfg(ctypes.Structure):
     """bi_loss_cfg"""
     _fields_ = [("variant", ctypes.c_int32), ("eps_low", ctypes.c_float), ("eps_high", ctypes.c_float),
                 ("gate", ctypes.c_float), ("flags", ctypes.c_int32)]
+
+
+class AdamWTensor(ctypes.Structure):
+    """bi_adamw_tensor"""
+    _fields_ = [("param", ctypes.c_void_p), ("master", ctypes.c_void_p), ("grad", ctypes.c_void_p),
+                ("exp_avg", ctypes.c_void_p), ("exp_avg_sq", ctypes.c_void_p), ("exp_avg_scale", ctypes.c_void_p),
+                ("exp_avg_sq_scale", ctypes.c_void_p), ("n", ctypes.c_int64)]
+
+
+class AdamWCfg(ctypes.Structure):
+    """bi_adamw_cfg"""
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double), ("step", ctypes.c_int64),
+                ("state_bits", ctypes.c_int32), ("param_bf16", ctypes.c_int32), ("grad_bf16", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
 
 
 LOSS_STORE_P = 1  # bi_loss_cfg.flags: BI_LOSS_STORE_P
@@ -79,5 +95,16 @@ def load() -> ctypes.CDLL:
     lib.bi_gemm_bf16.restype = ctypes.c_int
     lib.bi_rmsnorm.argtypes = [_p, _p, ctypes.c_float, _p, _i64, _i32, _p, _p]
     lib.bi_rmsnorm.restype = ctypes.c_int
+    f32 = ctypes.c_float
+    lib.bi_qk_norm_rope.argtypes = [_p, _p, _i64, _i64, _p, _p, _p, _p, f32, _i64, _i32, _i32, _i32, _i32, _p, _p,
+                                    _i64, _i64, _p, _p]
+    lib.bi_qk_norm_rope.restype = ctypes.c_int
+    lib.bi_qk_norm_rope_bwd_workspace_bytes.argtypes = [_i32]
+    lib.bi_qk_norm_rope_bwd_workspace_bytes.restype = _sz
+    lib.bi_qk_norm_rope_bwd.argtypes = [_p, _p, _i64, _i64, _p, _p, _i64, _i64, _p, _p, _p, _p, f32, _i64, _i32, _i32,
+                                        _i32, _i32, _p, _p, _i64, _i64, _p, _p, _p, _p, _sz, _p]
+    lib.bi_qk_norm_rope_bwd.restype = ctypes.c_int
+    lib.bi_adamw_step.argtypes = [_p, _i32, _p, _p, _p, _p, _p]
+    lib.bi_adamw_step.restype = ctypes.c_int
     _lib = lib
     return lib

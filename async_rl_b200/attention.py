@@ -1,0 +1,131 @@
+"""Binding of the attention layer's entry points (include/bi_model.h): the per-head norm with rotation
+and softmax attention, forward and backward.  Argument checks and marshalling only."""
+from __future__ import annotations
+
+import contextlib
+from typing import Optional
+
+import torch
+
+from . import _lib
+from .api import _ptr, _raise_host, _stream
+
+
+def _on(dev: torch.device):
+    """The tensors' device made current for the call (nothing to do where it already is)."""
+    if dev.index is None or dev.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(dev)
+
+
+def _need(t: torch.Tensor, name: str, dtype: torch.dtype, dev: torch.device, shape=None):
+    # the library dereferences every pointer on the GPU: host memory must never reach it
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor, got {t.device}")
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}, got {t.device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _rows(t: torch.Tensor, name: str, dev: torch.device, shape=None) -> int:
+    """Elements between the tokens of a [T, heads, D] bf16 tensor whose heads are contiguous."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor, got {t.device}")
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}, got {t.device}")
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.dim() != 3 or (shape is not None and t.shape != shape):
+        raise ValueError(f"{name} must be {list(shape) if shape is not None else '[T, heads, D]'}, got {list(t.shape)}")
+    T, H, D = t.shape
+    ld, sh, sd = t.stride()
+    if (D > 1 and sd != 1) or (H > 1 and sh != D):
+        raise ValueError(f"{name}: the heads of a token must be contiguous, strides are {t.stride()}")
+    if T <= 1:
+        return max(ld, H * D) if ld % 8 == 0 else -(-H * D // 8) * 8
+    return ld
+
+
+def _status(status: Optional[torch.Tensor], dev: torch.device) -> torch.Tensor:
+    if status is None:
+        return torch.empty(1, dtype=torch.int32, device=dev)
+    _need(status, "status", torch.int32, dev)
+    if status.numel() < 1:
+        raise ValueError("status must hold one element")
+    return status
+
+
+def _qk_common(q, k, gq, gk, positions, inv_freq, dev):
+    _rows(q, "q", dev)
+    T, Hq, D = q.shape
+    if k.dim() != 3 or k.shape[0] != T or k.shape[2] != D:
+        raise ValueError(f"k must be [{T}, heads, {D}], got {list(k.shape)}")
+    if (gq is None) != (gk is None):
+        raise ValueError("gq and gk are given together or not at all")
+    if gq is not None:
+        _need(gq, "gq", torch.bfloat16, dev, (D,))
+        _need(gk, "gk", torch.bfloat16, dev, (D,))
+    _need(positions, "positions", torch.int32, dev, (T,))
+    _need(inv_freq, "inv_freq", torch.float32, dev)
+    return T, Hq, k.shape[1], D, 2 * inv_freq.numel()
+
+
+def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, gq: Optional[torch.Tensor], gk: Optional[torch.Tensor],
+                 positions: torch.Tensor, inv_freq: torch.Tensor, eps: float, q_out: Optional[torch.Tensor] = None,
+                 k_out: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None):
+    """RMS norm of each head of q [T, Hq, D] and k [T, Hkv, D] with gains gq, gk [D] (None: no norm),
+    then the rotation of its position: pairs (i, i + R/2), i < R/2 = len(inv_freq), turned by
+    positions[t] * inv_freq[i]; elements past R pass (include/bi_model.h).  q and k may be slices of
+    one projection's output.  Returns (q_out, k_out, status [1] i32)."""
+    dev = q.device
+    T, Hq, Hkv, D, R = _qk_common(q, k, gq, gk, positions, inv_freq, dev)
+    q_ld, k_ld = _rows(q, "q", dev), _rows(k, "k", dev)
+    if q_out is None:
+        q_out = torch.empty(T, Hq, D, dtype=torch.bfloat16, device=dev)
+    if k_out is None:
+        k_out = torch.empty(T, Hkv, D, dtype=torch.bfloat16, device=dev)
+    qo_ld, ko_ld = _rows(q_out, "q_out", dev, q.shape), _rows(k_out, "k_out", dev, k.shape)
+    st = _status(status, dev)
+    with _on(dev):
+        code = _lib.load().bi_qk_norm_rope(_ptr(q), _ptr(k), q_ld, k_ld, _ptr(gq), _ptr(gk), _ptr(positions),
+                                           _ptr(inv_freq), float(eps), T, Hq, Hkv, D, R, _ptr(q_out), _ptr(k_out),
+                                           qo_ld, ko_ld, _ptr(st), _stream(dev))
+    _raise_host(code, "bi_qk_norm_rope")
+    return q_out, k_out, st
+
+
+def qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor,
+                     gq: Optional[torch.Tensor], gk: Optional[torch.Tensor], positions: torch.Tensor,
+                     inv_freq: torch.Tensor, eps: float, dq: Optional[torch.Tensor] = None,
+                     dk: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
+                     status: Optional[torch.Tensor] = None):
+    """The gradient of ``qk_norm_rope``.  Returns (dq, dk bf16, dgq, dgk [D] f32 or None, status)."""
+    dev = q.device
+    T, Hq, Hkv, D, R = _qk_common(q, k, gq, gk, positions, inv_freq, dev)
+    q_ld, k_ld = _rows(q, "q", dev), _rows(k, "k", dev)
+    gq_ld, gk_ld = _rows(dq_out, "dq_out", dev, q.shape), _rows(dk_out, "dk_out", dev, k.shape)
+    lib = _lib.load()
+    dgq = dgk = None
+    if gq is not None:
+        dgq, dgk = torch.empty(D, dtype=torch.float32, device=dev), torch.empty(D, dtype=torch.float32, device=dev)
+        if ws is None:
+            ws = torch.empty(max(lib.bi_qk_norm_rope_bwd_workspace_bytes(D), 256), dtype=torch.uint8, device=dev)
+        _need(ws, "ws", torch.uint8, dev)
+    if dq is None:
+        dq = torch.empty(T, Hq, D, dtype=torch.bfloat16, device=dev)
+    if dk is None:
+        dk = torch.empty(T, Hkv, D, dtype=torch.bfloat16, device=dev)
+    dq_ld, dk_ld = _rows(dq, "dq", dev, q.shape), _rows(dk, "dk", dev, k.shape)
+    st = _status(status, dev)
+    with _on(dev):
+        code = lib.bi_qk_norm_rope_bwd(_ptr(dq_out), _ptr(dk_out), gq_ld, gk_ld, _ptr(q), _ptr(k), q_ld, k_ld, _ptr(gq),
+                                       _ptr(gk), _ptr(positions), _ptr(inv_freq), float(eps), T, Hq, Hkv, D, R,
+                                       _ptr(dq), _ptr(dk), dq_ld, dk_ld, _ptr(dgq), _ptr(dgk), _ptr(st), _ptr(ws),
+                                       0 if ws is None else ws.numel(), _stream(dev))
+    _raise_host(code, "bi_qk_norm_rope_bwd")
+    return dq, dk, dgq, dgk, st

@@ -14,6 +14,7 @@
 
 #include "bi_isloss.h"
 #include "bi_model.h"
+#include "host.h"
 #include "kernels_decode.cuh"
 #include "kernels_dw.cuh"
 #include "kernels_lm.cuh"
@@ -24,72 +25,15 @@ namespace {
 
 using bi::Ctrl;
 using bi::RedPart;
+using namespace bi::host;
 
-constexpr uint64_t kWaitLimitNs = 4000000000ull;  // 4 s for any single in-kernel wait
+static_assert(sizeof(bi::D3Out) == sizeof(bi_d3), "device-written diagnostics match the ABI struct");
+
 constexpr size_t kZscanSmemMax = 200 * 1024;      // one row's partial sums in the decode combine
 constexpr int kMaxSms = 160;                      // upper bound used to size the dZ scratch
 constexpr int kDzSlotsMax = 2 * kMaxSms;          // clusters * C * slots-per-CTA <= 2 * SMs
 
 thread_local uint64_t g_force_timeout_ns = 0;
-
-// ---------------------------------------------------------------------------------------------
-// optional per-kernel timing (events around each launch; measurement tools only)
-// ---------------------------------------------------------------------------------------------
-enum KernelKind : int { kKPrep, kKRowmap, kKZeroRows, kKGather, kKLmFwd, kKLmFwdDH, kKLmDW, kKDwRows,
-                        kKDwStream, kKSeqGate, kKRowParts, kKReduce, kKD3Partial, kKGemm, kKRmsNorm, kKLmZscan,
-                        kKLmDecode1, kKD1Zero, kNumKinds };
-const char* const kKindNames[kNumKinds] = {"k_prep", "k_rowmap", "k_zero_prompt_rows", "k_gather_rows",
-                                           "k_lm_fwd", "k_lm_fwd_dh", "k_lm_dw", "k_dw_rows", "k_dw_stream",
-                                           "k_seq_gate", "k_row_parts", "k_reduce_parts", "k_d3_partial",
-                                           "k_gemm_pair", "k_rmsnorm", "k_lm_zscan", "k_lm_decode1",
-                                           "k_d1_zero"};
-static_assert(sizeof(bi::D3Out) == sizeof(bi_d3), "device-written diagnostics match the ABI struct");
-struct Pending {
-  int kind;
-  cudaEvent_t a, b;
-};
-struct Profiler {
-  bool on = false;
-  bool failed = false;
-  std::vector<Pending> pending;
-  std::vector<cudaEvent_t> pool;
-  double ms[kNumKinds] = {};
-  int64_t n[kNumKinds] = {};
-  cudaEvent_t get() {
-    if (!pool.empty()) {
-      cudaEvent_t e = pool.back();
-      pool.pop_back();
-      return e;
-    }
-    cudaEvent_t e = nullptr;
-    if (cudaEventCreate(&e) != cudaSuccess) failed = true;
-    return e;
-  }
-};
-thread_local Profiler g_prof;
-
-struct ProfScope {  // records an event pair around one launch when profiling is on
-  int kind;
-  cudaStream_t s;
-  cudaEvent_t a = nullptr;
-  ProfScope(int k, cudaStream_t st) : kind(k), s(st) {
-    if (g_prof.on) {
-      a = g_prof.get();
-      if (a) cudaEventRecord(a, s);
-    }
-  }
-  ~ProfScope() {
-    if (g_prof.on && a) {
-      cudaEvent_t b = g_prof.get();
-      if (b) {
-        cudaEventRecord(b, s);
-        g_prof.pending.push_back({kind, a, b});
-      }
-    }
-  }
-};
-
-size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 struct WsLayout {
   size_t ctrl, lse_c, g_c, tl_c, d3_c, delta_c, clip_c, y_c, logmu_c, rowmap, respof, coef, cprefix, rej, red, hc,
@@ -195,28 +139,9 @@ int cluster_split(int32_t H) {
   return 0;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 // ---------------------------------------------------------------------------------------------
-// tensor maps (driver entry point fetched through the runtime; no libcuda link dependency)
+// tensor maps
 // ---------------------------------------------------------------------------------------------
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(p);
-  });
-  return fn;
-}
-
 // 2-D bf16 row-major tensor [rows][cols], box {64 columns, box_rows rows}, 128-byte swizzle.
 bool make_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int box_rows) {
   EncodeTiledFn f = encode_fn();

@@ -1,0 +1,271 @@
+// kernels_adamw.cuh -- one AdamW step over many tensors, states in fp32 or in 8-bit blocks.
+//
+// The step is bound by HBM: 16 bytes of fp32 states (4 with 8-bit ones), the gradient, 8 bytes of
+// master weights and 2 of the bf16 copy an element, against about 16 operations.  A warp takes 256
+// consecutive elements at a time, eight a lane, so every lane's loads and stores are 8, 16 or 32
+// bytes wide and a block of the 8-bit states is one warp's: its two maxima are shuffles, with
+// nothing in shared memory.  The tensors' addresses travel as kernel parameters (at most 30 KB a
+// launch), so a call copies nothing to the device and can be captured.
+#pragma once
+
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+#include <cstdint>
+
+#include "bi_optim.h"
+#include "sm100.cuh"
+
+namespace bi {
+
+constexpr int kAdamThreads = 256;
+constexpr int kAdamUnit = 256;                      // elements of a warp's turn = a block of 8-bit states
+constexpr int kAdamUnitsPerWarp = 2;
+constexpr int kAdamChunk = kAdamUnit * kAdamUnitsPerWarp * (kAdamThreads / 32);  // elements of a block
+constexpr float kE4m3Max = 448.0f;
+constexpr float kE4m3Inv = 1.0f / 448.0f;
+constexpr float kE4m3Tiny = 0.001953125f;           // 2^-9, the smallest positive value
+
+struct AdamHyper {
+  float b1, c1, b2, c2;   // beta1, 1 - beta1, beta2, 1 - beta2
+  float rate, root, keep, eps;  // lr / (1 - beta1^t), 1 / sqrt(1 - beta2^t), 1 - lr wd, eps
+};
+struct AdamTensor {
+  void* p;
+  float* master;
+  const void* g;
+  void *m, *v;
+  float *ms, *vs;
+  int64_t n;
+};
+template <int kMax>
+struct AdamTable {
+  AdamTensor t[kMax];
+  uint32_t first[kMax + 1];  // first block of each tensor
+  uint32_t wide[(kMax + 31) / 32];  // bit i: tensor i's addresses allow vector access
+  int32_t count;
+};
+struct AdamArgs {
+  AdamHyper h;
+  double lr, beta1, beta2;
+  const float* grad_scale;
+  const int64_t* step_dev;
+  int32_t* status;
+  int32_t set_status;  // this launch is the call's first
+};
+
+struct F8 {
+  float x[8];
+};
+__device__ __forceinline__ F8 adam_ld_f32(const float* p) {
+  uint32_t r[8];
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "l"(p));
+  F8 f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) f.x[e] = __uint_as_float(r[e]);
+  return f;
+}
+__device__ __forceinline__ void adam_st_f32(float* p, const F8& f) {
+  uint32_t r[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) r[e] = __float_as_uint(f.x[e]);
+  st_global_v8(p, r);
+}
+__device__ __forceinline__ float bf16_up(uint32_t bits) { return __uint_as_float(bits << 16); }
+__device__ __forceinline__ F8 adam_ld_bf16(const uint16_t* p) {
+  uint32_t r[4];
+  asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "l"(p));
+  F8 f;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    f.x[2 * e] = bf16_up(r[e] & 0xffffu);
+    f.x[2 * e + 1] = __uint_as_float(r[e] & 0xffff0000u);
+  }
+  return f;
+}
+__device__ __forceinline__ void adam_st_bf16(uint16_t* p, const F8& f) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(f.x[0], f.x[1]), pack_bf16x2(f.x[2], f.x[3]),
+                                            pack_bf16x2(f.x[4], f.x[5]), pack_bf16x2(f.x[6], f.x[7]));
+}
+__device__ __forceinline__ float e4m3_up(uint32_t code) {
+  const __half_raw h = __nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(code), __NV_E4M3);
+  return __half2float(__half(h));
+}
+__device__ __forceinline__ uint32_t e4m3_down(float x) {
+  return __nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3);
+}
+
+// One element; every operation is rounded, none contracted, so a plain evaluation in the same order
+// gives the same bits (and with 8-bit states the same codes).
+__device__ __forceinline__ void adam_one(const AdamHyper& h, float gs, float g, float& p, float& m, float& v) {
+  g = __fmul_rn(g, gs);  // gs = 1 without a grad_scale: exact
+  m = __fadd_rn(__fmul_rn(m, h.b1), __fmul_rn(g, h.c1));
+  v = __fadd_rn(__fmul_rn(v, h.b2), __fmul_rn(__fmul_rn(g, g), h.c2));
+  const float den = __fadd_rn(__fmul_rn(__fsqrt_rn(v), h.root), h.eps);
+  p = __fsub_rn(__fmul_rn(p, h.keep), __fdiv_rn(__fmul_rn(m, h.rate), den));
+}
+
+__device__ __forceinline__ float adam_warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
+// kState8: 8-bit states; kPBf16: bf16 params; kMaster: with fp32 masters; kGBf16: bf16 gradients
+template <int kMax, bool kState8, bool kPBf16, bool kMaster, bool kGBf16>
+__global__ void __launch_bounds__(kAdamThreads) k_adamw(const __grid_constant__ AdamTable<kMax> tab, const AdamArgs a) {
+  __shared__ AdamHyper sh;
+  AdamHyper h = a.h;
+  if (a.step_dev) {
+    const int64_t t = *a.step_dev;
+    if (t < 1) {
+      if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = 1 /* BI_ERR_INVALID_ARG */;
+      return;
+    }
+    if (threadIdx.x == 0) {
+      h.rate = static_cast<float>(a.lr / (1.0 - pow(a.beta1, static_cast<double>(t))));
+      h.root = static_cast<float>(1.0 / sqrt(1.0 - pow(a.beta2, static_cast<double>(t))));
+      sh = h;
+    }
+    __syncthreads();
+    h = sh;
+  }
+  if (a.set_status && blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0;
+  const float gs = a.grad_scale ? *a.grad_scale : 1.0f;
+  // the block's tensor: the last one whose first block is not behind this one
+  int lo = 0, hi = tab.count - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) / 2;
+    if (tab.first[mid] <= blockIdx.x)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  const AdamTensor& t = tab.t[lo];
+  const bool wide = (tab.wide[lo / 32] >> (lo % 32)) & 1u;
+  const int64_t n = t.n;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t base = static_cast<int64_t>(blockIdx.x - tab.first[lo]) * kAdamChunk + warp * kAdamUnit;
+  float* pf = kMaster ? t.master : static_cast<float*>(t.p);
+  uint16_t* pb = static_cast<uint16_t*>(t.p);
+  const float* gf = static_cast<const float*>(t.g);
+  const uint16_t* gb = static_cast<const uint16_t*>(t.g);
+#pragma unroll
+  for (int u = 0; u < kAdamUnitsPerWarp; ++u) {
+    const int64_t unit = base + static_cast<int64_t>(u) * (kAdamThreads / 32) * kAdamUnit;
+    const int64_t i0 = unit + lane * 8;
+    if (unit >= n) break;  // the whole warp
+    const bool full = wide && i0 + 8 <= n;
+    F8 p, g, m, v;
+    const int64_t block = unit / kAdamUnit;
+    if (full) {
+      g = kGBf16 ? adam_ld_bf16(gb + i0) : adam_ld_f32(gf + i0);
+      p = (kPBf16 && !kMaster) ? adam_ld_bf16(pb + i0) : adam_ld_f32(pf + i0);
+      if (!kState8) {
+        m = adam_ld_f32(static_cast<const float*>(t.m) + i0);
+        v = adam_ld_f32(static_cast<const float*>(t.v) + i0);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int64_t i = i0 + e;
+        const bool in = i < n;
+        g.x[e] = !in ? 0.f : kGBf16 ? bf16_up(gb[i]) : gf[i];
+        p.x[e] = !in ? 0.f : (kPBf16 && !kMaster) ? bf16_up(pb[i]) : pf[i];
+        if (!kState8) {
+          m.x[e] = in ? static_cast<const float*>(t.m)[i] : 0.f;
+          v.x[e] = in ? static_cast<const float*>(t.v)[i] : 0.f;
+        }
+      }
+    }
+    if (kState8) {
+      const uint8_t* mc = static_cast<const uint8_t*>(t.m) + i0;
+      const uint8_t* vc = static_cast<const uint8_t*>(t.v) + i0;
+      uint32_t mw[2] = {}, vw[2] = {};
+      if (full) {
+        const uint2 x = *reinterpret_cast<const uint2*>(mc), y = *reinterpret_cast<const uint2*>(vc);
+        mw[0] = x.x, mw[1] = x.y, vw[0] = y.x, vw[1] = y.y;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (i0 + e < n) {
+            mw[e / 4] |= static_cast<uint32_t>(mc[e]) << (8 * (e % 4));
+            vw[e / 4] |= static_cast<uint32_t>(vc[e]) << (8 * (e % 4));
+          }
+      }
+      const float sm = t.ms[block], sv = t.vs[block];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        m.x[e] = __fmul_rn(e4m3_up((mw[e / 4] >> (8 * (e % 4))) & 0xffu), sm);
+        const float r = __fmul_rn(e4m3_up((vw[e / 4] >> (8 * (e % 4))) & 0xffu), sv);
+        v.x[e] = __fmul_rn(r, r);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) adam_one(h, gs, g.x[e], p.x[e], m.x[e], v.x[e]);
+    if (kState8) {
+      float mm = 0.f, mv = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        v.x[e] = __fsqrt_rn(v.x[e]);
+        if (i0 + e < n) {
+          mm = fmaxf(mm, fabsf(m.x[e]));
+          mv = fmaxf(mv, v.x[e]);
+        }
+      }
+      mm = adam_warp_max(mm);
+      mv = adam_warp_max(mv);
+      // a subnormal maximum's reciprocal would be infinite; sqrt(v) is never that small
+      const float im = mm > 0.f ? fminf(__fmul_rn(__frcp_rn(mm), kE4m3Max), 3.4028235e38f) : 0.f;
+      const float iv = mv > 0.f ? __fmul_rn(__frcp_rn(mv), kE4m3Max) : 0.f;
+      uint32_t mw[2] = {}, vw[2] = {};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        float r = __fmul_rn(v.x[e], iv);
+        if (v.x[e] > 0.f) r = fmaxf(r, kE4m3Tiny);
+        mw[e / 4] |= e4m3_down(__fmul_rn(m.x[e], im)) << (8 * (e % 4));
+        vw[e / 4] |= e4m3_down(r) << (8 * (e % 4));
+      }
+      uint8_t* mc = static_cast<uint8_t*>(t.m) + i0;
+      uint8_t* vc = static_cast<uint8_t*>(t.v) + i0;
+      if (full) {
+        *reinterpret_cast<uint2*>(mc) = make_uint2(mw[0], mw[1]);
+        *reinterpret_cast<uint2*>(vc) = make_uint2(vw[0], vw[1]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (i0 + e < n) {
+            mc[e] = static_cast<uint8_t>(mw[e / 4] >> (8 * (e % 4)));
+            vc[e] = static_cast<uint8_t>(vw[e / 4] >> (8 * (e % 4)));
+          }
+      }
+      if (lane == 0) {
+        t.ms[block] = __fmul_rn(mm, kE4m3Inv);
+        t.vs[block] = __fmul_rn(mv, kE4m3Inv);
+      }
+    }
+    if (full) {
+      if (kPBf16) adam_st_bf16(pb + i0, p);
+      if (!kPBf16 || kMaster) adam_st_f32(pf + i0, p);
+      if (!kState8) {
+        adam_st_f32(static_cast<float*>(t.m) + i0, m);
+        adam_st_f32(static_cast<float*>(t.v) + i0, v);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int64_t i = i0 + e;
+        if (i >= n) continue;
+        if (kPBf16) pb[i] = static_cast<uint16_t>(pack_bf16x2(p.x[e], 0.f) & 0xffffu);
+        if (!kPBf16 || kMaster) pf[i] = p.x[e];
+        if (!kState8) {
+          static_cast<float*>(t.m)[i] = m.x[e];
+          static_cast<float*>(t.v)[i] = v.x[e];
+        }
+      }
+    }
+  }
+}
+
+}  // namespace bi

@@ -1,0 +1,130 @@
+"""Binding of the AdamW step (include/bi_optim.h).  Argument checks and marshalling only."""
+from __future__ import annotations
+
+import ctypes
+from typing import List, Optional, Sequence, Union
+
+import torch
+
+from . import _lib
+from .api import _ptr, _raise_host, _stream
+from .attention import _on, _status
+
+STATE_BLOCK = 256  # elements that share a scale in the 8-bit states
+
+
+def _flat(ts, name, n, dtype, dev, sizes=None):
+    if len(ts) != n:
+        raise ValueError(f"{name} has {len(ts)} tensors, params has {n}")
+    for i, t in enumerate(ts):
+        if not t.is_cuda or t.device != dev:
+            raise ValueError(f"{name}[{i}] must be a CUDA tensor on {dev}, got {t.device}")
+        if t.dtype != dtype:
+            raise ValueError(f"{name}[{i}] must be {dtype}, got {t.dtype}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name}[{i}] must be contiguous")
+        if sizes is not None and t.numel() != sizes[i]:
+            raise ValueError(f"{name}[{i}] must have {sizes[i]} elements, got {t.numel()}")
+
+
+class AdamWState:
+    """The tensors that ``adamw_step`` updates, checked once.
+
+    ``params``: float32 or bfloat16, all of one type.  ``masters``: float32 weights of bfloat16 params
+    (the update is made there and rounded into the param), or None.  ``exp_avg``, ``exp_avg_sq``:
+    float32, or float8_e4m3fn with ``exp_avg_scale`` and ``exp_avg_sq_scale`` (float32, one for each
+    256 elements): then m = exp_avg * scale and sqrt(v) = exp_avg_sq * scale."""
+
+    def __init__(self, params: Sequence[torch.Tensor], masters: Optional[Sequence[torch.Tensor]],
+                 exp_avg: Sequence[torch.Tensor], exp_avg_sq: Sequence[torch.Tensor],
+                 exp_avg_scale: Optional[Sequence[torch.Tensor]] = None,
+                 exp_avg_sq_scale: Optional[Sequence[torch.Tensor]] = None):
+        n = len(params)
+        if n == 0:
+            raise ValueError("params is empty")
+        self.device = params[0].device
+        if params[0].dtype not in (torch.float32, torch.bfloat16):
+            raise ValueError(f"params must be float32 or bfloat16, got {params[0].dtype}")
+        self.param_bf16 = params[0].dtype == torch.bfloat16
+        self.sizes = [p.numel() for p in params]
+        self.shapes = [p.shape for p in params]
+        _flat(params, "params", n, params[0].dtype, self.device)
+        if masters is not None:
+            if not self.param_bf16:
+                raise ValueError("masters are for bfloat16 params")
+            _flat(masters, "masters", n, torch.float32, self.device, self.sizes)
+        if (exp_avg_scale is None) != (exp_avg_sq_scale is None):
+            raise ValueError("exp_avg_scale and exp_avg_sq_scale are given together or not at all")
+        self.state_bits = 32 if exp_avg_scale is None else 8
+        held = torch.float32 if self.state_bits == 32 else torch.float8_e4m3fn
+        _flat(exp_avg, "exp_avg", n, held, self.device, self.sizes)
+        _flat(exp_avg_sq, "exp_avg_sq", n, held, self.device, self.sizes)
+        if self.state_bits == 8:
+            blocks = [-(-s // STATE_BLOCK) for s in self.sizes]
+            _flat(exp_avg_scale, "exp_avg_scale", n, torch.float32, self.device, blocks)
+            _flat(exp_avg_sq_scale, "exp_avg_sq_scale", n, torch.float32, self.device, blocks)
+        self.params, self.masters = list(params), None if masters is None else list(masters)
+        self.exp_avg, self.exp_avg_sq = list(exp_avg), list(exp_avg_sq)
+        self.exp_avg_scale = None if exp_avg_scale is None else list(exp_avg_scale)
+        self.exp_avg_sq_scale = None if exp_avg_sq_scale is None else list(exp_avg_sq_scale)
+        spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in self.tensors() if t.numel())
+        for (_, end), (start, _) in zip(spans, spans[1:]):
+            if start < end:
+                raise ValueError("the tensors of one step may not overlap")
+
+    @staticmethod
+    def allocate(params: Sequence[torch.Tensor], state_bits: int = 32, master: bool = False) -> "AdamWState":
+        """States of zeros for ``params`` and, with ``master``, float32 copies of bfloat16 params."""
+        if state_bits not in (8, 32):
+            raise ValueError(f"state_bits must be 8 or 32, got {state_bits}")
+        held = torch.float32 if state_bits == 32 else torch.float8_e4m3fn
+        zeros = lambda: [torch.zeros(p.shape, dtype=torch.uint8 if state_bits == 8 else held,  # noqa: E731
+                                     device=p.device).view(held) for p in params]
+        scale = lambda: [torch.zeros(-(-p.numel() // STATE_BLOCK), device=p.device) for p in params]  # noqa: E731
+        return AdamWState(params, [p.detach().float() for p in params] if master else None, zeros(), zeros(),
+                          scale() if state_bits == 8 else None, scale() if state_bits == 8 else None)
+
+    def tensors(self) -> List[torch.Tensor]:
+        """Every tensor that a step reads and writes, the gradients apart."""
+        lists = (self.params, self.masters, self.exp_avg, self.exp_avg_sq, self.exp_avg_scale, self.exp_avg_sq_scale)
+        return [t for ts in lists if ts is not None for t in ts]
+
+
+def adamw_step(state: AdamWState, grads: Sequence[torch.Tensor], step: Union[int, torch.Tensor], lr: float,
+               beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8, weight_decay: float = 0.01,
+               grad_scale: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None):
+    """One AdamW step, in place, over all tensors of ``state`` (include/bi_optim.h).  ``grads``: one
+    contiguous float32 or bfloat16 tensor (all of one type) for each param, of its shape.  ``step`` counts
+    from 1; as a CUDA int64 tensor it is read when the kernel runs, so that a captured step can be
+    replayed.  ``grad_scale``: a CUDA float32 scalar that multiplies the gradients.  Returns status."""
+    dev = state.device
+    n = len(state.params)
+    if len(grads) != n:
+        raise ValueError(f"grads has {len(grads)} tensors, params has {n}")
+    gt = grads[0].dtype
+    if gt not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"grads must be float32 or bfloat16, got {gt}")
+    for i, (g, shape) in enumerate(zip(grads, state.shapes)):
+        if not g.is_cuda or g.device != dev or g.dtype != gt or g.shape != shape or not g.is_contiguous():
+            raise ValueError(f"grads[{i}] must be a contiguous {gt} CUDA tensor of shape {list(shape)} on {dev}, got "
+                             f"{g.dtype} {list(g.shape)} on {g.device}")
+    step_dev = None
+    if isinstance(step, torch.Tensor):
+        if not step.is_cuda or step.device != dev or step.dtype != torch.int64 or step.numel() != 1:
+            raise ValueError(f"step must be an int or a CUDA int64 tensor of one element on {dev}")
+        step_dev, step = step, 0
+    if grad_scale is not None and (not grad_scale.is_cuda or grad_scale.device != dev or
+                                   grad_scale.dtype != torch.float32 or grad_scale.numel() != 1):
+        raise ValueError(f"grad_scale must be a CUDA float32 tensor of one element on {dev}")
+    st = _status(status, dev)
+    ptrs = lambda ts: (0,) * n if ts is None else [t.data_ptr() for t in ts]  # noqa: E731
+    table = (_lib.AdamWTensor * n)(*zip(ptrs(state.params), ptrs(state.masters), ptrs(grads), ptrs(state.exp_avg),
+                                        ptrs(state.exp_avg_sq), ptrs(state.exp_avg_scale),
+                                        ptrs(state.exp_avg_sq_scale), state.sizes))
+    cfg = _lib.AdamWCfg(float(lr), float(beta1), float(beta2), float(eps), float(weight_decay), int(step),
+                        state.state_bits, int(state.param_bf16), int(gt == torch.bfloat16), 0)
+    with _on(dev):
+        code = _lib.load().bi_adamw_step(ctypes.addressof(table), n, ctypes.addressof(cfg), _ptr(grad_scale),
+                                         _ptr(step_dev), _ptr(st), _stream(dev))
+    _raise_host(code, "bi_adamw_step")
+    return st

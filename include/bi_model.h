@@ -1,7 +1,8 @@
 /*
- * bi_model.h -- C ABI of the batch-invariant dense layers of the policy model: the bf16 GEMM of a
- * linear layer and RMSNorm.  Same library (libbi_isloss.so), status codes and conventions as
- * bi_isloss.h.
+ * bi_model.h -- C ABI of the batch-invariant layers of the policy model: the bf16 GEMM of a linear
+ * layer, RMSNorm, and the attention layer's parts: the norm of each query and key head with its
+ * rotation, and softmax attention, both with their backward passes.  Same library
+ * (libbi_isloss.so), status codes and conventions as bi_isloss.h.
  *
  * Sources (page titles and sections):
  *   "Zero Mismatch, Simple Async RL", section "Only one probability gap comes from old weights":
@@ -61,6 +62,44 @@ BI_API bi_status bi_gemm_bf16(const uint16_t* x, const uint16_t* w, uint16_t* y,
  */
 BI_API bi_status bi_rmsnorm(const uint16_t* x, const uint16_t* g, float eps, uint16_t* y, int64_t M, int32_t H,
                             int32_t* dev_status, void* stream);
+
+/*
+ * RMS norm of each query and key head, and the rotation of its position, in one pass.  With x one
+ * head's D values, y = x / sqrt(mean(x^2) + eps) * g (gq for q's heads, gk for k's), and for i < R/2
+ * and the angle a_i = position * inv_freq_i:
+ *   z_i         = y_i cos a_i - y_{i+R/2} sin a_i
+ *   z_{i + R/2} = y_{i+R/2} cos a_i + y_i sin a_i
+ * and z = y past R.  gq = gk = NULL: y = x (rotation only).
+ *   q [T][Hq][D], k [T][Hkv][D] bf16: heads are D apart, tokens q_ld and k_ld elements (slices of one
+ *     projection's output are fine); 16-byte aligned, q_ld >= Hq D and k_ld >= Hkv D multiples of 8
+ *   gq, gk [D] bf16, 16-byte aligned;  positions [T] int32 (any value);  inv_freq [R / 2] float
+ *   q_out, k_out: the same layouts with their own token strides; may not overlap q or k
+ *   0 <= T < 2^31;  Hq, Hkv in 1..4096;  D a multiple of 16 and <= 256;  R a multiple of 16, 0 < R <= D
+ * Arithmetic: fp32, one rounding to bf16; the angles in turns in fp64, so that far positions keep
+ * their phase.  A head's output depends on its own input, position and gains only.
+ * Returns BI_ERR_INVALID_ARG for a NULL, misaligned or aliased pointer, a bad stride, or a negative or
+ * non-finite eps; BI_ERR_UNSUPPORTED_SHAPE for Hq, Hkv, D or R; BI_ERR_CUDA when the launch fails.
+ */
+BI_API bi_status bi_qk_norm_rope(const uint16_t* q, const uint16_t* k, int64_t q_ld, int64_t k_ld, const uint16_t* gq,
+                                 const uint16_t* gk, const int32_t* positions, const float* inv_freq, float eps,
+                                 int64_t T, int32_t Hq, int32_t Hkv, int32_t D, int32_t R, uint16_t* q_out,
+                                 uint16_t* k_out, int64_t q_out_ld, int64_t k_out_ld, int32_t* dev_status,
+                                 void* stream);
+
+/*
+ * Its gradient: dq, dk (bf16, laid out like q, k with their own token strides) and, with gains,
+ * dgq, dgk [D] float, overwritten (zeros for T = 0).  dq_out, dk_out: gradients of q_out and k_out;
+ * q, k: the inputs (not read without gains, and may then be NULL).  dq and dk may not overlap an input.
+ * The gains' gradients are added up in a fixed order for a given T (no atomics): the same call gives
+ * the same bits.  ws: bi_qk_norm_rope_bwd_workspace_bytes(D) bytes, 256-byte aligned (gains only).
+ */
+BI_API size_t bi_qk_norm_rope_bwd_workspace_bytes(int32_t D);
+BI_API bi_status bi_qk_norm_rope_bwd(const uint16_t* dq_out, const uint16_t* dk_out, int64_t dq_out_ld,
+                                     int64_t dk_out_ld, const uint16_t* q, const uint16_t* k, int64_t q_ld,
+                                     int64_t k_ld, const uint16_t* gq, const uint16_t* gk, const int32_t* positions,
+                                     const float* inv_freq, float eps, int64_t T, int32_t Hq, int32_t Hkv, int32_t D,
+                                     int32_t R, uint16_t* dq, uint16_t* dk, int64_t dq_ld, int64_t dk_ld, float* dgq,
+                                     float* dgk, int32_t* dev_status, void* ws, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }
