@@ -129,3 +129,59 @@ def qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: torch.Tensor, q: torch.Tensor
                                        0 if ws is None else ws.numel(), _stream(dev))
     _raise_host(code, "bi_qk_norm_rope_bwd")
     return dq, dk, dgq, dgk, st
+
+
+def _attn_common(q, k, v, q_offsets, k_offsets, k_lens, scale, dev):
+    """(S, scale, k_offsets, q_ld, k_ld, v_ld) after the checks that forward and backward share."""
+    q_ld, k_ld = _rows(q, "q", dev), _rows(k, "k", dev)
+    v_ld = _rows(v, "v", dev, k.shape)
+    if k.shape[2] != q.shape[2]:
+        raise ValueError(f"q has heads of {q.shape[2]}, k of {k.shape[2]}")
+    _need(q_offsets, "q_offsets", torch.int64, dev)
+    S = q_offsets.numel() - 1
+    if q_offsets.dim() != 1 or S < 0:
+        raise ValueError("q_offsets must be [S + 1]")
+    if k_offsets is None:
+        if k.shape[0] != q.shape[0]:
+            raise ValueError(f"k has {k.shape[0]} rows and q {q.shape[0]}: give k_offsets")
+        k_offsets = q_offsets
+    else:
+        _need(k_offsets, "k_offsets", torch.int64, dev, q_offsets.shape)
+    if k_lens is not None:
+        _need(k_lens, "k_lens", torch.int32, dev, (S,))
+    return S, float(q.shape[2] ** -0.5 if scale is None else scale), k_offsets, q_ld, k_ld, v_ld
+
+
+def attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_offsets: torch.Tensor,
+             k_offsets: Optional[torch.Tensor] = None, k_lens: Optional[torch.Tensor] = None, causal: bool = True,
+             scale: Optional[float] = None, ws: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+             lse: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None):
+    """Softmax attention of q [Tq, Hq, D] over k, v [Tk, Hkv, D] (include/bi_model.h).  Sequence s has the
+    query rows q_offsets[s]:q_offsets[s+1] and the key rows from k_offsets[s] on, k_lens[s] of them (all up
+    to k_offsets[s+1] without k_lens); without k_offsets the keys are packed as the queries are.  Under
+    ``causal`` the queries are the last positions of their sequence.  ``scale`` defaults to D ** -0.5.
+    Rows in no sequence are left as they were.  Returns (out [Tq, Hq, D] bf16, lse [Hq, Tq] f32, status)."""
+    dev = q.device
+    S, scale, k_offsets, q_ld, k_ld, v_ld = _attn_common(q, k, v, q_offsets, k_offsets, k_lens, scale, dev)
+    Tq, Hq, D = q.shape
+    Tk, Hkv = k.shape[0], k.shape[1]
+    lib = _lib.load()
+    if ws is None:
+        ws = torch.empty(max(lib.bi_attn_fwd_workspace_bytes(Tq, Tk, S, Hq, Hkv, D), 256), dtype=torch.uint8, device=dev)
+    else:
+        _need(ws, "ws", torch.uint8, dev)
+    if out is None:
+        out = torch.empty(Tq, Hq, D, dtype=torch.bfloat16, device=dev)
+    else:
+        _need(out, "out", torch.bfloat16, dev, q.shape)
+    if lse is None:
+        lse = torch.empty(Hq, Tq, dtype=torch.float32, device=dev)
+    else:
+        _need(lse, "lse", torch.float32, dev, (Hq, Tq))
+    st = _status(status, dev)
+    with _on(dev):
+        code = lib.bi_attn_fwd(_ptr(q), _ptr(k), _ptr(v), q_ld, k_ld, v_ld, _ptr(q_offsets), _ptr(k_offsets),
+                               _ptr(k_lens), S, Tq, Tk, Hq, Hkv, D, 1 if causal else 0, scale, _ptr(out), _ptr(lse),
+                               _ptr(st), _ptr(ws), ws.numel(), _stream(dev))
+    _raise_host(code, "bi_attn_fwd")
+    return out, lse, st

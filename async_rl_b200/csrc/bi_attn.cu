@@ -1,0 +1,203 @@
+// bi_attn.cu -- entry points of softmax attention (include/bi_model.h).
+#include <cmath>
+
+#include "bi_model.h"
+#include "host.h"
+#include "kernels_attn.cuh"
+
+namespace {
+
+using namespace bi::host;
+
+constexpr int kMaxSms = 160;
+constexpr size_t kPartBytesMax = size_t{128} << 20;  // partial rows of a split forward, at most
+
+struct Shape {
+  int64_t Tq, Tk;
+  int32_t S, Hq, Hkv, D;
+  int32_t G, tpt;
+};
+
+bool shape_ok(Shape& z) {
+  if (z.Hq <= 0 || z.Hkv <= 0 || z.Hq % z.Hkv != 0 || z.Hq / z.Hkv > bi::kAtTile || z.Hkv > 4096) return false;
+  if (z.D != 64 && z.D != 128) return false;
+  z.G = z.Hq / z.Hkv;
+  z.tpt = bi::kAtTile / z.G;
+  return true;
+}
+bool sizes_ok(const Shape& z) {
+  return z.Tq >= 0 && z.Tk >= 0 && z.S >= 0 && z.Tq < (int64_t{1} << 31) - 512 && z.Tk < (int64_t{1} << 31) - 512;
+}
+bool rows_ok(const void* p, int64_t ld, int32_t heads, int32_t D) {
+  return p && aligned16(p) && ld >= static_cast<int64_t>(heads) * D && ld % 8 == 0;
+}
+
+// Workspace of the forward.  Partial rows are provided where the rows alone would leave SMs without
+// work (fewer than four row tiles an SM), for sequences of up to twice the mean number of queries;
+// where that is not enough the plan does not split, and the results are the same.
+struct FwdLayout {
+  size_t head, seqs, units, scratch, part, part_ml, total;
+  int64_t cap_part;
+  int32_t cap_units;
+};
+FwdLayout fwd_layout(const Shape& z) {
+  FwdLayout L{};
+  const int64_t S = z.S > 0 ? z.S : 1;
+  const bool chunks = z.Tk > bi::kAtChunk;
+  if (chunks && z.Tq * z.Hq < int64_t{4} * kMaxSms * bi::kAtTile) {
+    const int64_t row = static_cast<int64_t>(z.Hq) * (z.D + 2) * 4;
+    const int64_t want = 2 * ((z.Tq + S - 1) / S) * (S + z.Tk / bi::kAtChunk);
+    const int64_t most = static_cast<int64_t>(kPartBytesMax) / row;
+    L.cap_part = want < most ? want : most;
+  }
+  L.cap_units = static_cast<int32_t>(S + z.Tq / (2 * z.tpt) + 1 + L.cap_part);
+  size_t o = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = o;
+    o = align_up(o + bytes, 256);
+    return at;
+  };
+  L.head = take(sizeof(bi::AttnPlanHead));
+  L.seqs = take(static_cast<size_t>(S) * sizeof(bi::AttnSeq));
+  L.units = take(static_cast<size_t>(L.cap_units) * sizeof(bi::AttnUnit));
+  L.scratch = take(chunks ? static_cast<size_t>(kMaxSms) * 2 * z.D * bi::kAtTile * 4 : 0);
+  L.part = take(static_cast<size_t>(L.cap_part) * z.Hq * z.D * 4);
+  L.part_ml = take(static_cast<size_t>(L.cap_part) * z.Hq * 8);
+  L.total = o;
+  return L;
+}
+
+// [T][heads][D] bf16 with `ld` elements between tokens, box {64 columns, box_heads, box_rows}.
+bool make_map_heads(CUtensorMap* m, const void* base, int64_t T, int32_t heads, int32_t D, int64_t ld, int box_heads,
+                    int box_rows) {
+  EncodeTiledFn f = encode_fn();
+  if (!f) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(heads),
+                              static_cast<cuuint64_t>(T > 0 ? T : 1)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(ld) * 2};
+  const cuuint32_t box[3] = {64u, static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t estr[3] = {1u, 1u, 1u};
+  return f(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The current device's SM count, with the kernels' shared memory granted once.
+int attn_device() {
+  static std::mutex mu;
+  static int ready[64] = {};
+  int dev = 0;
+  const int sms = sm_count();
+  if (sms <= 0 || sms > kMaxSms || cudaGetDevice(&dev) != cudaSuccess) return 0;
+  std::lock_guard<std::mutex> lk(mu);
+  if (!ready[dev]) {
+    if (cudaFuncSetAttribute(bi::k_attn_fwd<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             bi::AtFwdTile<128>::smem + bi::kAtSharedBytes) != cudaSuccess ||
+        cudaFuncSetAttribute(bi::k_attn_fwd<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             bi::AtFwdTile<64>::smem + bi::kAtSharedBytes) != cudaSuccess)
+      return 0;
+    ready[dev] = 1;
+  }
+  return sms;
+}
+
+template <int D>
+bool launch_fwd(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const bi::AttnFwdArgs& a,
+                unsigned grid, bool join, int32_t S, int sms, cudaStream_t s) {
+  {
+    ProfScope ps(kKAttnFwd, s);
+    bi::k_attn_fwd<D><<<grid, bi::kAtFwdThreads, bi::AtFwdTile<D>::smem + bi::kAtSharedBytes, s>>>(mq, mk, mv, a);
+  }
+  if (join) {
+    const int64_t want = (a.Tq * a.Hq + bi::kAtJoinThreads / 32 - 1) / (bi::kAtJoinThreads / 32);
+    const int64_t cap = static_cast<int64_t>(sms) * 16;
+    ProfScope ps(kKAttnJoin, s);
+    bi::k_attn_join<D><<<static_cast<unsigned>(want < cap ? want : cap), bi::kAtJoinThreads, 0, s>>>(a, S);
+  }
+  return cudaGetLastError() == cudaSuccess;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t bi_attn_fwd_workspace_bytes(int64_t Tq, int64_t Tk, int32_t S, int32_t Hq, int32_t Hkv, int32_t D) {
+  Shape z{Tq, Tk, S, Hq, Hkv, D, 0, 0};
+  if (!sizes_ok(z) || !shape_ok(z)) return 0;
+  return fwd_layout(z).total;
+}
+
+bi_status bi_attn_fwd(const uint16_t* q, const uint16_t* k, const uint16_t* v, int64_t q_ld, int64_t k_ld, int64_t v_ld,
+                      const int64_t* q_offsets, const int64_t* k_offsets, const int32_t* k_lens, int32_t S, int64_t Tq,
+                      int64_t Tk, int32_t Hq, int32_t Hkv, int32_t D, int32_t causal, float scale, uint16_t* out,
+                      float* lse, int32_t* dev_status, void* ws, size_t ws_bytes, void* stream) {
+  Shape z{Tq, Tk, S, Hq, Hkv, D, 0, 0};
+  if (!dev_status || !sizes_ok(z) || !(scale > 0.f) || !std::isfinite(scale)) return BI_ERR_INVALID_ARG;
+  if (!shape_ok(z)) return BI_ERR_UNSUPPORTED_SHAPE;
+  if (S > 0 && (!q_offsets || !k_offsets)) return BI_ERR_INVALID_ARG;
+  if (Tq > 0 && (!rows_ok(q, q_ld, Hq, D) || !out || !aligned16(out) || !lse)) return BI_ERR_INVALID_ARG;
+  if (Tk > 0 && (!rows_ok(k, k_ld, Hkv, D) || !rows_ok(v, v_ld, Hkv, D))) return BI_ERR_INVALID_ARG;
+  const FwdLayout L = fwd_layout(z);
+  if (!ws || ws_bytes < L.total || (reinterpret_cast<uintptr_t>(ws) & 255u)) return BI_ERR_WORKSPACE;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (S == 0 || Tq == 0) return cudaMemsetAsync(dev_status, 0, sizeof(int32_t), s) == cudaSuccess ? BI_OK : BI_ERR_CUDA;
+  const int sms = attn_device();
+  if (sms <= 0) return BI_ERR_CUDA;
+  uint8_t* w8 = static_cast<uint8_t*>(ws);
+  bi::AttnPlanArgs p{};
+  p.qo = q_offsets;
+  p.ko = k_offsets;
+  p.kl = k_lens;
+  p.Tq = Tq;
+  p.Tk = Tk;
+  p.S = S;
+  p.mode = bi::kPlanFwd;
+  p.causal = causal != 0;
+  p.step = 2 * z.tpt;
+  p.tpt = z.tpt;
+  p.sms = sms;
+  p.Hkv = Hkv;
+  p.cap_units = L.cap_units;
+  p.cap_part = L.cap_part;
+  p.seqs = reinterpret_cast<bi::AttnSeq*>(w8 + L.seqs);
+  p.units = reinterpret_cast<bi::AttnUnit*>(w8 + L.units);
+  p.head = reinterpret_cast<bi::AttnPlanHead*>(w8 + L.head);
+  p.status = dev_status;
+  // a call without keys reads none of them: any address serves the maps
+  CUtensorMap mq, mk, mv;
+  const void* kb = Tk > 0 ? static_cast<const void*>(k) : ws;
+  const void* vb = Tk > 0 ? static_cast<const void*>(v) : ws;
+  const int64_t kl = Tk > 0 ? k_ld : static_cast<int64_t>(Hkv) * D, vl = Tk > 0 ? v_ld : static_cast<int64_t>(Hkv) * D;
+  if (!make_map_heads(&mq, q, Tq, Hq, D, q_ld, z.G, z.tpt) || !make_map_heads(&mk, kb, Tk, Hkv, D, kl, 1, bi::kAtTile) ||
+      !make_map_heads(&mv, vb, Tk, Hkv, D, vl, 1, bi::kAtTile))
+    return BI_ERR_CUDA;
+  {
+    ProfScope ps(kKAttnPlan, s);
+    bi::k_attn_plan<<<1, bi::kPlanThreads, 0, s>>>(p, p);
+  }
+  bi::AttnFwdArgs a{};
+  a.seqs = p.seqs;
+  a.units = p.units;
+  a.head = p.head;
+  a.out = out;
+  a.lse = lse;
+  a.scratch = reinterpret_cast<float*>(w8 + L.scratch);
+  a.part = reinterpret_cast<float*>(w8 + L.part);
+  a.part_ml = reinterpret_cast<float2*>(w8 + L.part_ml);
+  a.Tq = Tq;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.G = z.G;
+  a.tpt = z.tpt;
+  a.causal = p.causal;
+  a.c = scale * bi::kLog2e;
+  a.status = dev_status;
+  a.limit_ns = kWaitLimitNs;
+  const int64_t most = static_cast<int64_t>(L.cap_units) * Hkv;
+  const unsigned grid = static_cast<unsigned>(most < sms ? most : sms);
+  const bool ok = D == 128 ? launch_fwd<128>(mq, mk, mv, a, grid, L.cap_part > 0, S, sms, s)
+                           : launch_fwd<64>(mq, mk, mv, a, grid, L.cap_part > 0, S, sms, s);
+  return ok ? BI_OK : BI_ERR_CUDA;
+}
+
+}  // extern "C"

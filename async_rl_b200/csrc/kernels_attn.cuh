@@ -1,0 +1,715 @@
+// kernels_attn.cuh -- softmax attention over packed sequences or key/value caches: the work plan and
+// the forward pass.
+//
+// Mathematics.  For a query row with scores s_j = q . k_j (j over its visible keys) and
+// c = scale log2(e), one pass over the keys keeps a reference m and
+//   l = sum_j 2^(c s_j - m),   O = sum_j 2^(c s_j - m) v_j,
+// multiplying l and O by 2^(m - m') when the reference is raised to m'.  out = O / l and
+// lse = (m + log2 l) ln 2.  The reference follows the running maximum lazily: it is raised only by a
+// tile whose maximum is more than 8 above it (every term stays below 2^8), which after the first
+// tile of a row is rare.
+//
+// Fixed chunks.  The keys of a sequence are cut into chunks of 2048, counted from its first key.  A
+// chunk starts from m = -inf, and chunks are joined in order:
+//   m' = max(m, m_c),  O' = O 2^(m - m') + O_c 2^(m_c - m'),  l' likewise.
+// Tiles of 128 keys, chunks and the order of every sum depend on the key's place in its sequence
+// only, so a row's output has the same bits in a prefill, in a decode step over a cache and in any
+// batch; a long cache with few rows is worked on by many SMs, one chunk each, joined by a second
+// kernel with the same expressions.
+//
+// Rows.  The G = Hq / Hkv query heads of one key/value head share its keys: a tile of 128 rows holds
+// floor(128 / G) tokens times G heads, so a decode step fills its tile with the group's heads and
+// every key tile is read once for all of them.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <cstdint>
+
+#include "kernels_lm.cuh"
+
+namespace bi {
+
+constexpr int kAtTile = 128;                          // rows and keys of a tile
+constexpr int kAtChunkTiles = 16;
+constexpr int kAtChunk = kAtTile * kAtChunkTiles;     // keys of a chunk
+
+struct AttnSeq {
+  int64_t q0, k0;    // first query and key row
+  int64_t part0;     // first of its partial rows (tokens x chunks), split forward only
+  int32_t lq, lk;    // queries and keys
+  int32_t unit0;     // first of its units before splitting
+  int32_t nch;       // chunks of its keys, at least 1
+};
+struct AttnUnit {
+  int32_t seq;
+  int32_t t0;        // first query (forward, dQ) or key (dK, dV) of the unit
+  int32_t c0, c1;    // chunks [c0, c1) (forward)
+};
+struct AttnPlanHead {
+  int32_t nunits;
+  int32_t split;     // units are single chunks; rows of sequences with several are joined later
+};
+
+// ----------------------------------------------------------------------------------------------
+// plan: check the offsets, cut the sequences into units and list them, longest first
+// ----------------------------------------------------------------------------------------------
+enum AttnPlanMode : int { kPlanFwd = 0, kPlanDq = 1, kPlanDkv = 2 };
+struct AttnPlanArgs {
+  const int64_t *qo, *ko;
+  const int32_t* kl;       // or NULL
+  int64_t Tq, Tk;
+  int32_t S, mode, causal;
+  int32_t step;            // queries (keys) of a unit
+  int32_t tpt;             // tokens of a 128-row tile
+  int32_t sms, Hkv;
+  int32_t cap_units;
+  int64_t cap_part;        // partial rows the workspace holds
+  AttnSeq* seqs;
+  AttnUnit* units;
+  AttnPlanHead* head;
+  int32_t* status;         // written where not NULL
+};
+
+// Key tiles that the queries [.., last] see, and query tiles that see keys from `first` on.
+__host__ __device__ __forceinline__ int32_t attn_visible(int32_t tok, int32_t lq, int32_t lk, int32_t causal) {
+  const int32_t v = causal ? tok + lk - lq + 1 : lk;
+  return v < 0 ? 0 : (v > lk ? lk : v);
+}
+__host__ __device__ __forceinline__ int32_t attn_first_query(int32_t key, int32_t lq, int32_t lk, int32_t causal) {
+  const int32_t i = causal ? key - (lk - lq) : 0;
+  return i < 0 ? 0 : i;
+}
+__device__ __forceinline__ int32_t attn_cost(const AttnPlanArgs& a, int32_t lq, int32_t lk, int32_t t0) {
+  if (a.mode == kPlanDkv) {
+    const int32_t first = attn_first_query(t0, lq, lk, a.causal);
+    return first >= lq ? 0 : (lq + a.tpt - 1) / a.tpt - first / a.tpt;
+  }
+  const int32_t last = (t0 + a.step < lq ? t0 + a.step : lq) - 1;
+  return (attn_visible(last, lq, lk, a.causal) + kAtTile - 1) / kAtTile;
+}
+
+constexpr int kPlanThreads = 1024;
+
+// Inclusive scan over the block; `carry` is added and the block's total left in *total.
+__device__ __forceinline__ int64_t plan_scan(int64_t v, int64_t* warp_sums, int64_t* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t n = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += n;
+  }
+  __syncthreads();  // the previous scan's readers are done
+  if (lane == 31) warp_sums[warp] = v;
+  __syncthreads();
+  if (warp == 0) {
+    int64_t w = warp_sums[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t n = __shfl_up_sync(0xffffffffu, w, o);
+      if (lane >= o) w += n;
+    }
+    warp_sums[lane] = w;
+  }
+  __syncthreads();
+  *total = warp_sums[31];
+  return v + (warp > 0 ? warp_sums[warp - 1] : 0);
+}
+
+__global__ void __launch_bounds__(kPlanThreads) k_attn_plan(const AttnPlanArgs p0, const AttnPlanArgs p1) {
+  const AttnPlanArgs& a = blockIdx.x == 0 ? p0 : p1;
+  __shared__ int64_t warp_sums[32];
+  __shared__ int32_t hist[kPlanThreads];
+  __shared__ int32_t longest;
+  __shared__ unsigned long long work;
+  const int tid = threadIdx.x;
+  if (tid == 0) longest = 0, work = 0;
+  hist[tid] = 0;
+  __syncthreads();
+  int64_t units = 0, parts = 0, split_units = 0;
+  int bad = 0;
+  for (int64_t base = 0; base < a.S; base += kPlanThreads) {
+    const int64_t s = base + tid;
+    int64_t n = 0, pr = 0, su = 0;
+    AttnSeq q{};
+    if (s < a.S) {
+      const int64_t q0 = a.qo[s], q1 = a.qo[s + 1], k0 = a.ko[s], k1 = a.ko[s + 1];
+      const int64_t lk = a.kl ? static_cast<int64_t>(a.kl[s]) : k1 - k0;
+      if (q0 < 0 || q1 < q0 || q1 > a.Tq || k0 < 0 || k1 < k0 || k1 > a.Tk || lk < 0 || lk > k1 - k0) {
+        bad = 1;
+      } else {
+        q.q0 = q0;
+        q.k0 = k0;
+        q.lq = static_cast<int32_t>(q1 - q0);
+        q.lk = static_cast<int32_t>(lk);
+        q.nch = q.lk > kAtChunk ? (q.lk + kAtChunk - 1) / kAtChunk : 1;
+        const int32_t len = a.mode == kPlanDkv ? q.lk : q.lq;
+        n = (len + a.step - 1) / a.step;
+        if (a.mode == kPlanFwd) {
+          pr = q.nch > 1 ? static_cast<int64_t>(q.lq) * q.nch : 0;
+          su = n * q.nch;
+        }
+        if (n > 0) {
+          const int32_t c0 = attn_cost(a, q.lq, q.lk, 0);
+          const int32_t c1 = attn_cost(a, q.lq, q.lk, static_cast<int32_t>((n - 1) * a.step));
+          atomicMax(&longest, c0 > c1 ? c0 : c1);
+          atomicAdd(&work, static_cast<unsigned long long>(n) * (c0 + c1) / 2);
+        }
+      }
+    }
+    int64_t tn, tp, ts;
+    const int64_t en = plan_scan(n, warp_sums, &tn) - n + units;
+    const int64_t ep = plan_scan(pr, warp_sums, &tp) - pr + parts;
+    plan_scan(su, warp_sums, &ts);
+    if (s < a.S) {
+      q.unit0 = static_cast<int32_t>(en);
+      q.part0 = ep;
+      a.seqs[s] = q;
+    }
+    units += tn;
+    parts += tp;
+    split_units += ts;
+  }
+  bad = __syncthreads_or(bad);
+  if (bad) {
+    if (tid == 0) {
+      a.head->nunits = 0;
+      a.head->split = 0;
+      if (a.status) *a.status = 8 /* BI_ERR_BAD_OFFSETS */;
+    }
+    return;
+  }
+  // Splitting pays where the longest unit is a large part of an SM's share of the work: there the
+  // other SMs would wait for it.  It costs a write and a read of the partial rows.
+  const bool split = a.mode == kPlanFwd && parts > 0 && parts <= a.cap_part && split_units <= a.cap_units &&
+                     2ull * static_cast<unsigned long long>(longest) * a.sms > work * static_cast<unsigned long long>(a.Hkv);
+  // counting sort by cost, dearest first; the order within a cost is free (it decides which SM
+  // works on a unit, never a result)
+  for (int pass = 0; pass < 2; ++pass) {
+    for (int64_t i = tid; i < units; i += kPlanThreads) {
+      int32_t lo = 0, hi = a.S - 1;
+      while (lo < hi) {  // the last sequence whose first unit is not behind i
+        const int32_t mid = lo + (hi - lo + 1) / 2;
+        if (a.seqs[mid].unit0 <= i)
+          lo = mid;
+        else
+          hi = mid - 1;
+      }
+      const AttnSeq& q = a.seqs[lo];
+      const int32_t t0 = static_cast<int32_t>(i - q.unit0) * a.step;
+      const int32_t cost = attn_cost(a, q.lq, q.lk, t0);
+      const int32_t nc = split ? (cost + kAtChunkTiles - 1) / kAtChunkTiles : 1;
+      for (int32_t c = 0; c < (nc > 0 ? nc : 1); ++c) {
+        const int32_t left = cost - c * kAtChunkTiles;
+        int32_t w = split && left > kAtChunkTiles ? kAtChunkTiles : left;
+        w = w < kPlanThreads - 1 ? w : kPlanThreads - 1;
+        const int32_t at = atomicAdd(&hist[w], 1);
+        if (pass == 1) a.units[at] = AttnUnit{lo, t0, split ? c : 0, split ? c + 1 : 0x7fffffff / kAtChunkTiles};
+      }
+    }
+    __syncthreads();
+    if (pass == 0) {
+      const int32_t w = kPlanThreads - 1 - tid;
+      const int64_t n = hist[w];
+      int64_t total;
+      const int64_t e = plan_scan(n, warp_sums, &total) - n;
+      hist[w] = static_cast<int32_t>(e);
+      if (tid == 0) {
+        a.head->nunits = static_cast<int32_t>(total);
+        a.head->split = split ? 1 : 0;
+        if (a.status) *a.status = 0;
+      }
+      __syncthreads();
+    }
+  }
+}
+
+// ----------------------------------------------------------------------------------------------
+// forward
+// ----------------------------------------------------------------------------------------------
+struct AttnFwdArgs {
+  const AttnSeq* seqs;
+  const AttnUnit* units;
+  const AttnPlanHead* head;
+  uint16_t* out;       // [Tq][Hq][D]
+  float* lse;          // [Hq][Tq]
+  float* scratch;      // [CTAs][2][D / 4][128][4]: running O of tiles with several chunks
+  float* part;         // [partial rows][Hq][D]
+  float2* part_ml;     // [partial rows][Hq]: (m, l)
+  int64_t Tq;
+  int32_t Hq, Hkv, G, tpt;
+  int32_t causal;
+  float c;             // scale log2(e)
+  int32_t* status;
+  uint64_t limit_ns;
+};
+
+constexpr int kAtFwdThreads = 320;  // warps 0-3 and 4-7: softmax of the two row tiles; 8: TMA; 9: MMA
+
+template <int D>
+struct AtFwdTile {
+  static constexpr int tile_bytes = kAtTile * D * 2;       // Q, K and V tiles: D / 64 blocks of [128][64]
+  static constexpr int slots = D == 128 ? 5 : 8;           // ring of K and V tiles
+  static constexpr int smem = (2 + slots) * tile_bytes;
+};
+struct AtFwdShared {
+  uint64_t full[8], empty[8];
+  uint64_t q_full, q_empty;
+  uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t done;
+  uint32_t tmem_base;
+  volatile uint32_t abort_flag;
+};
+constexpr int kAtSharedBytes = static_cast<int>((sizeof(AtFwdShared) + 127) / 128 * 128);
+
+__device__ __forceinline__ float attn_join_scale(float from, float to) {
+  return to == -INFINITY ? 0.f : ex2_approx(from - to);
+}
+
+// What every role derives from a unit.
+struct AtUnit {
+  AttnSeq q;
+  int32_t h;        // key/value head
+  int32_t t0;
+  int32_t jb;       // first key tile
+  int32_t je[2];    // end of each row tile's key tiles
+  int32_t n;        // end of the unit's
+};
+__device__ __forceinline__ AtUnit at_unit(const AttnFwdArgs& a, int64_t u) {
+  AtUnit x;
+  const AttnUnit w = a.units[u / a.Hkv];
+  x.h = static_cast<int32_t>(u % a.Hkv);
+  x.q = a.seqs[w.seq];
+  x.t0 = w.t0;
+  x.jb = w.c0 * kAtChunkTiles;
+#pragma unroll
+  for (int X = 0; X < 2; ++X) {
+    const int32_t first = w.t0 + X * a.tpt;
+    int32_t last = first + a.tpt;
+    last = (last < x.q.lq ? last : x.q.lq) - 1;
+    const int32_t n = last < first ? 0 : (attn_visible(last, x.q.lq, x.q.lk, a.causal) + kAtTile - 1) / kAtTile;
+    x.je[X] = n < w.c1 * kAtChunkTiles ? n : w.c1 * kAtChunkTiles;
+  }
+  x.n = x.je[0] > x.je[1] ? x.je[0] : x.je[1];
+  return x;
+}
+
+template <int D>
+__device__ __forceinline__ void at_fwd_load(AtFwdShared& sh, const AttnFwdArgs& a, uint32_t smem, int64_t nu,
+                                            const CUtensorMap* mq, const CUtensorMap* mk, const CUtensorMap* mv) {
+  using T = AtFwdTile<D>;
+  const WaitCtl wc{&sh.abort_flag, a.status, a.limit_ns};
+  tma_prefetch_desc(mq);
+  tma_prefetch_desc(mk);
+  tma_prefetch_desc(mv);
+  const uint32_t ring = smem + 2 * T::tile_bytes;
+  const uint32_t qbytes = static_cast<uint32_t>(a.tpt * a.G) * 128u * (D / 64);
+  uint32_t slot = 0, phase = 0, qph = 0;
+  for (int64_t u = blockIdx.x; u < nu; u += gridDim.x) {
+    const AtUnit x = at_unit(a, u);
+    if (x.n <= x.jb) continue;
+    if (!mbar_wait<false>(&sh.q_empty, qph ^ 1u, wc)) return;
+    qph ^= 1u;
+    const int nx = x.je[1] > x.jb ? 2 : 1;
+    mbar_arrive_expect_tx(&sh.q_full, qbytes * nx);
+    for (int X = 0; X < nx; ++X)
+#pragma unroll
+      for (int b = 0; b < D / 64; ++b)
+        tma_load_3d(smem + X * T::tile_bytes + b * kAUnitBytes, mq, &sh.q_full, b * 64, x.h * a.G,
+                    static_cast<int32_t>(x.q.q0) + x.t0 + X * a.tpt);
+    for (int32_t j = x.jb; j < x.n; ++j) {
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        if (!mbar_wait<false>(&sh.empty[slot], phase ^ 1u, wc)) return;
+        mbar_arrive_expect_tx(&sh.full[slot], T::tile_bytes);
+#pragma unroll
+        for (int b = 0; b < D / 64; ++b)
+          tma_load_3d(ring + slot * T::tile_bytes + b * kAUnitBytes, kv ? mv : mk, &sh.full[slot], b * 64, x.h,
+                      static_cast<int32_t>(x.q.k0) + j * kAtTile);
+        ring_advance(slot, phase, T::slots);
+      }
+    }
+  }
+}
+
+// Rows [valid, 128) of a tile in shared memory become zeros (the whole warp): what lies behind a
+// sequence's last key may be another sequence's or never written, and 0 x NaN would reach every row.
+template <int D>
+__device__ __forceinline__ void at_zero_rows(uint8_t* tile, int valid) {
+  const int lane = threadIdx.x & 31;
+  for (int r = valid + (lane >> 3); r < kAtTile; r += 4)
+#pragma unroll
+    for (int b = 0; b < D / 64; ++b)
+      *reinterpret_cast<uint4*>(tile + b * kAUnitBytes + r * 128 + (lane & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+  fence_proxy_async_shared();
+  __syncwarp();
+}
+
+template <int D>
+__device__ __forceinline__ void at_fwd_mma(AtFwdShared& sh, const AttnFwdArgs& a, uint8_t* smem_p, int64_t nu,
+                                           uint32_t tmem) {
+  using T = AtFwdTile<D>;
+  const WaitCtl wc{&sh.abort_flag, a.status, a.limit_ns};
+  const uint32_t smem = smem_u32(smem_p);
+  const int lane = threadIdx.x & 31;
+  constexpr uint32_t idesc_s = idesc_bf16(128, 128, false, false);
+  constexpr uint32_t idesc_o = idesc_bf16(128, D, false, true);
+  constexpr uint64_t blk = kAUnitBytes >> 4;
+  const uint64_t dq0 = sdesc_k_sw128(smem);
+  const uint64_t dk0 = sdesc_k_sw128(smem + 2 * T::tile_bytes);
+  const uint64_t dv0 = sdesc_mn_sw128(smem + 2 * T::tile_bytes, kAUnitBytes);
+  uint32_t slot = 0, phase = 0, qph = 0, pph[2] = {0, 0};
+  auto scores = [&](int X, uint32_t ks) {  // S_X = Q_X K^T
+    if (lane == 0) {
+      const uint64_t da = dq0 + X * (T::tile_bytes >> 4), db = dk0 + ks * (T::tile_bytes >> 4);
+#pragma unroll
+      for (int b = 0; b < D / 64; ++b)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          umma_bf16(tmem + X * 128, da + b * blk + 2 * k, db + b * blk + 2 * k, idesc_s, (b | k) ? 1u : 0u);
+      umma_commit(&sh.s_full[X]);
+    }
+  };
+  auto values = [&](int X, uint32_t vs, bool first) {  // O_X += P_X V
+    if (lane == 0) {
+      const uint64_t db = dv0 + vs * (T::tile_bytes >> 4);
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        umma_bf16_ta(tmem + 256 + X * D, tmem + X * 128 + k * 8, db + k * (2048 >> 4), idesc_o,
+                     (k > 0 || !first) ? 1u : 0u);
+    }
+  };
+  for (int64_t u = blockIdx.x; u < nu; u += gridDim.x) {
+    const AtUnit x = at_unit(a, u);
+    if (x.n <= x.jb) continue;
+    if (!__all_sync(0xffffffffu, mbar_wait<false>(&sh.q_full, qph, wc))) break;
+    qph ^= 1u;
+    if (!__all_sync(0xffffffffu, mbar_wait<false>(&sh.full[slot], phase, wc))) break;
+    tc_fence_after();
+    for (int X = 0; X < 2; ++X)
+      if (x.jb < x.je[X]) scores(X, slot);
+    if (lane == 0) {
+      umma_commit(&sh.empty[slot]);
+      if (x.jb + 1 == x.n) umma_commit(&sh.q_empty);
+    }
+    ring_advance(slot, phase, T::slots);
+    bool ok = true;
+    for (int32_t j = x.jb; j < x.n; ++j) {
+      const uint32_t vs = slot, vph = phase;
+      ring_advance(slot, phase, T::slots);
+      if (!__all_sync(0xffffffffu, mbar_wait<false>(&sh.full[vs], vph, wc))) { ok = false; break; }
+      const int32_t rows = x.q.lk - j * kAtTile;
+      if (rows < kAtTile) at_zero_rows<D>(smem_p + (2 + vs) * T::tile_bytes, rows);
+      const bool next = j + 1 < x.n;
+      const bool first = j % kAtChunkTiles == 0;
+      const bool last = (j + 1) % kAtChunkTiles == 0;
+      bool have_k = false;
+#pragma unroll
+      for (int X = 0; X < 2; ++X) {
+        if (j < x.je[X]) {
+          if (!__all_sync(0xffffffffu, mbar_wait<false>(&sh.p_full[X], pph[X], wc))) { ok = false; break; }
+          pph[X] ^= 1u;
+          tc_fence_after();
+          values(X, vs, first);
+          if (lane == 0 && (last || j + 1 == x.je[X])) umma_commit(&sh.o_full[X]);
+        }
+        if (next && !have_k) {
+          if (!__all_sync(0xffffffffu, mbar_wait<false>(&sh.full[slot], phase, wc))) { ok = false; break; }
+          tc_fence_after();
+          have_k = true;
+        }
+        if (j + 1 < x.je[X]) scores(X, slot);
+      }
+      if (!ok) break;
+      if (lane == 0) {
+        umma_commit(&sh.empty[vs]);
+        if (next) umma_commit(&sh.empty[slot]);
+        if (j + 2 == x.n) umma_commit(&sh.q_empty);
+      }
+      if (next) ring_advance(slot, phase, T::slots);
+    }
+    if (!ok) break;
+  }
+  __syncwarp();
+  if (lane == 0) umma_commit(&sh.done);
+  mbar_wait<false>(&sh.done, 0u, wc);
+}
+
+// Softmax and output of row tile X (128 threads, one row each).
+template <int D>
+__device__ __forceinline__ void at_fwd_softmax(AtFwdShared& sh, const AttnFwdArgs& a, int X, int64_t nu, bool split,
+                                               uint32_t tmem) {
+  const WaitCtl wc{&sh.abort_flag, a.status, a.limit_ns};
+  const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
+  const int row = warp * 32 + lane;
+  const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+  const uint32_t ts = tmem + X * 128 + lanes, to = tmem + 256 + X * D + lanes;
+  const int tok_in = row / a.G, g = row - tok_in * a.G;
+  float4* scr = reinterpret_cast<float4*>(a.scratch) + ((static_cast<int64_t>(blockIdx.x) * 2 + X) * (D / 4)) * 128 + row;
+  uint32_t sph = 0, oph = 0;
+  for (int64_t u = blockIdx.x; u < nu; u += gridDim.x) {
+    const AtUnit x = at_unit(a, u);
+    const int32_t tok = x.t0 + X * a.tpt + tok_in;
+    const bool valid = tok_in < a.tpt && tok < x.q.lq;
+    const bool warp_valid = __any_sync(0xffffffffu, valid);
+    const int32_t vis = valid ? attn_visible(tok, x.q.lq, x.q.lk, a.causal) : 0;
+    const int32_t head = x.h * a.G + g;
+    uint16_t* out = a.out + ((x.q.q0 + tok) * a.Hq + head) * D;
+    float* lse = a.lse + static_cast<int64_t>(head) * a.Tq + x.q.q0 + tok;
+    const bool joined = split && x.q.nch > 1;  // k_attn_join writes the rows of this sequence
+    if (x.je[X] <= x.jb) {
+      if (valid && !joined) {  // no key to see
+#pragma unroll
+        for (int e = 0; e < D / 8; ++e) reinterpret_cast<uint4*>(out)[e] = make_uint4(0u, 0u, 0u, 0u);
+        *lse = -INFINITY;
+      }
+      continue;
+    }
+    float m = -INFINITY, l = 0.f;          // of the chunk
+    float m_run = -INFINITY, l_run = 0.f;  // of the chunks before
+    for (int32_t j = x.jb; j < x.je[X]; ++j) {
+      if (!__all_sync(0xffffffffu, mbar_wait<false>(&sh.s_full[X], sph, wc))) return;
+      sph ^= 1u;
+      tc_fence_after();
+      const bool first = j % kAtChunkTiles == 0;
+      if (first) m = -INFINITY, l = 0.f;
+      if (warp_valid) {
+        uint32_t s[4][32];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) tmem_ld32(ts + b * 32, s[b]);
+        tmem_ld_wait();
+#pragma unroll
+        for (int b = 0; b < 4; ++b) tmem_ld_pin(s[b]);
+        const int32_t lim = vis - j * kAtTile;
+        if (__any_sync(0xffffffffu, lim < kAtTile)) {
+#pragma unroll
+          for (int b = 0; b < 4; ++b)
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (b * 32 + e >= lim) s[b][e] = 0xff800000u;  // -inf
+        }
+        float mx[4];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          mx[b] = __uint_as_float(s[b][0]);
+#pragma unroll
+          for (int e = 1; e < 32; ++e) mx[b] = fmaxf(mx[b], __uint_as_float(s[b][e]));
+        }
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.c;
+        if (first) {
+          m = top;
+        } else {
+          const bool raise = top > m + 8.f;
+          if (__any_sync(0xffffffffu, raise)) {
+            // S of this tile was issued behind the last product into O: O is complete
+            const float alpha = raise ? attn_join_scale(m, top) : 1.f;
+            if (raise) m = top;
+            l *= alpha;
+#pragma unroll 1
+            for (int b = 0; b < D / 32; ++b) {
+              uint32_t o[32];
+              tmem_ld32(to + b * 32, o);
+              tmem_ld_wait();
+              tmem_ld_pin(o);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+              tmem_st32(to + b * 32, o);
+            }
+          }
+        }
+        const float mu = m == -INFINITY ? 0.f : -m;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int b = 0; b < 4; b += 2) {
+          uint32_t p[32];
+#pragma unroll
+          for (int e = 0; e < 64; e += 2) {
+            const float p0 = ex2_approx(fmaf(__uint_as_float(s[b + e / 32][e % 32]), a.c, mu));
+            const float p1 = ex2_approx(fmaf(__uint_as_float(s[b + e / 32][e % 32 + 1]), a.c, mu));
+            sum[(e / 2) % 2 * 2] += p0;
+            sum[(e / 2) % 2 * 2 + 1] += p1;
+            p[e / 2] = pack_bf16x2(p0, p1);  // bf16 terms: what the tensor cores take; l keeps fp32
+          }
+          tmem_st32(ts + b * 16, p);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        tmem_st_wait();
+      }
+      tc_fence_before();
+      mbar_arrive(&sh.p_full[X]);
+      const bool last = j + 1 == x.je[X];
+      if (!last && (j + 1) % kAtChunkTiles != 0) continue;
+      // the chunk's end
+      if (!__all_sync(0xffffffffu, mbar_wait<false>(&sh.o_full[X], oph, wc))) return;
+      oph ^= 1u;
+      tc_fence_after();
+      if (!warp_valid) continue;
+      const bool fresh = j - x.jb < kAtChunkTiles;  // no chunk before it in this unit
+      if (joined) {
+        const int64_t pr = (x.q.part0 + static_cast<int64_t>(tok) * x.q.nch + j / kAtChunkTiles) * a.Hq + head;
+        const bool mine = valid && vis > j / kAtChunkTiles * kAtChunk;
+        if (mine) a.part_ml[pr] = make_float2(m, l);
+#pragma unroll 1
+        for (int b = 0; b < D / 32; ++b) {
+          uint32_t o[32];
+          tmem_ld32(to + b * 32, o);
+          tmem_ld_wait();
+          tmem_ld_pin(o);
+          if (mine)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) st_global_v8(a.part + pr * D + b * 32 + e * 8, o + e * 8);
+        }
+        continue;
+      }
+      const float m_new = fmaxf(m_run, m);
+      const float ka = fresh ? 0.f : attn_join_scale(m_run, m_new), kb = fresh ? 1.f : attn_join_scale(m, m_new);
+      l_run = fresh ? l : fmaf(l, kb, l_run * ka);
+      m_run = m_new;
+      const float inv = l_run > 0.f || l_run != l_run ? 1.f / l_run : 0.f;
+#pragma unroll 1
+      for (int b = 0; b < D / 32; ++b) {
+        uint32_t o[32];
+        tmem_ld32(to + b * 32, o);
+        tmem_ld_wait();
+        tmem_ld_pin(o);
+        if (!fresh) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float4 r = scr[(b * 8 + e) * 128];
+            o[4 * e] = __float_as_uint(fmaf(__uint_as_float(o[4 * e]), kb, r.x * ka));
+            o[4 * e + 1] = __float_as_uint(fmaf(__uint_as_float(o[4 * e + 1]), kb, r.y * ka));
+            o[4 * e + 2] = __float_as_uint(fmaf(__uint_as_float(o[4 * e + 2]), kb, r.z * ka));
+            o[4 * e + 3] = __float_as_uint(fmaf(__uint_as_float(o[4 * e + 3]), kb, r.w * ka));
+          }
+        }
+        if (!last) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            scr[(b * 8 + e) * 128] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
+                                                 __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
+        } else if (valid) {
+          uint32_t p[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            p[e] = pack_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            *reinterpret_cast<uint4*>(out + b * 32 + e * 8) =
+                make_uint4(p[4 * e], p[4 * e + 1], p[4 * e + 2], p[4 * e + 3]);
+        }
+      }
+      if (last && valid) *lse = m_run == -INFINITY ? -INFINITY : fmaf(m_run, 0.69314718055994531f, logf(l_run));
+    }
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kAtFwdThreads, 1)
+    k_attn_fwd(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+               const __grid_constant__ CUtensorMap mv, const AttnFwdArgs a) {
+  // mq: Q [Tq][Hq][D], box {64, G, tpt}; mk, mv: [Tk][Hkv][D], box {64, 1, 128}; 128-byte swizzle
+  extern __shared__ __align__(1024) uint8_t dsmem[];
+  AtFwdShared& sh = *reinterpret_cast<AtFwdShared*>(dsmem + AtFwdTile<D>::smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 8; ++i) {
+      mbar_init(&sh.full[i], 1);
+      mbar_init(&sh.empty[i], 1);
+    }
+    mbar_init(&sh.q_full, 1);
+    mbar_init(&sh.q_empty, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.p_full[i], 128);
+      mbar_init(&sh.o_full[i], 1);
+    }
+    mbar_init(&sh.done, 1);
+    sh.abort_flag = 0u;
+    fence_mbar_init_cluster();
+  }
+  if (warp == 9) {
+    tmem_alloc(&sh.tmem_base, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem_base;
+  const uint32_t smem = smem_u32(dsmem);
+  const bool misaligned = (smem & 1023u) != 0;
+  if (misaligned && threadIdx.x == 0) raise_status(a.status, 4 /* BI_ERR_CUDA */);
+  const int64_t nu = misaligned ? 0 : static_cast<int64_t>(a.head->nunits) * a.Hkv;
+  const bool split = a.head->split != 0;
+  if (warp < 8) {
+    at_fwd_softmax<D>(sh, a, warp >> 2, nu, split, tmem);
+  } else if (warp == 8) {
+    if (lane == 0) at_fwd_load<D>(sh, a, smem, nu, &mq, &mk, &mv);
+    __syncwarp();
+  } else {
+    at_fwd_mma<D>(sh, a, dsmem, nu, tmem);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (sh.abort_flag != 0u) {  // on the error path a copy or a commit may still be in flight
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 50000u) {
+    }
+  }
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the chunks of split rows, a warp a row: the expressions of the forward's own joining.
+constexpr int kAtJoinThreads = 128;
+template <int D>
+__global__ void __launch_bounds__(kAtJoinThreads)
+    k_attn_join(const AttnFwdArgs a, const int32_t S) {
+  if (a.head->split == 0 || a.head->nunits == 0) return;
+  const int lane = threadIdx.x & 31;
+  constexpr int N = D / 32;
+  const int64_t rows = a.Tq * a.Hq;
+  const int64_t nw = static_cast<int64_t>(gridDim.x) * (kAtJoinThreads / 32);
+  for (int64_t r = (static_cast<int64_t>(blockIdx.x) * kAtJoinThreads + threadIdx.x) >> 5; r < rows; r += nw) {
+    const int64_t t = r / a.Hq;
+    const int32_t head = static_cast<int32_t>(r - t * a.Hq);
+    int32_t lo = 0, hi = S - 1;
+    while (lo < hi) {
+      const int32_t mid = lo + (hi - lo + 1) / 2;
+      if (a.seqs[mid].q0 <= t)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    const AttnSeq q = a.seqs[lo];
+    const int64_t tok = t - q.q0;
+    if (q.nch <= 1 || tok < 0 || tok >= q.lq) continue;
+    const int32_t vis = attn_visible(static_cast<int32_t>(tok), q.lq, q.lk, a.causal);
+    const int32_t nch = (vis + kAtChunk - 1) / kAtChunk;
+    float m_run = -INFINITY, l_run = 0.f, o[N];
+#pragma unroll
+    for (int e = 0; e < N; ++e) o[e] = 0.f;
+    for (int32_t c = 0; c < nch; ++c) {
+      const int64_t pr = (q.part0 + tok * q.nch + c) * a.Hq + head;
+      const float2 ml = a.part_ml[pr];
+      const float m_new = fmaxf(m_run, ml.x);
+      const float ka = c == 0 ? 0.f : attn_join_scale(m_run, m_new), kb = c == 0 ? 1.f : attn_join_scale(ml.x, m_new);
+      l_run = c == 0 ? ml.y : fmaf(ml.y, kb, l_run * ka);
+      m_run = m_new;
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        const float v = a.part[pr * D + e * 32 + lane];
+        o[e] = c == 0 ? v : fmaf(v, kb, o[e] * ka);
+      }
+    }
+    const float inv = l_run > 0.f || l_run != l_run ? 1.f / l_run : 0.f;
+    uint16_t* out = a.out + r * D;
+#pragma unroll
+    for (int e = 0; e < N; ++e) out[e * 32 + lane] = static_cast<uint16_t>(pack_bf16x2(o[e] * inv, 0.f) & 0xffffu);
+    if (lane == 0)
+      a.lse[static_cast<int64_t>(head) * a.Tq + t] =
+          m_run == -INFINITY ? -INFINITY : fmaf(m_run, 0.69314718055994531f, logf(l_run));
+  }
+}
+
+}  // namespace bi

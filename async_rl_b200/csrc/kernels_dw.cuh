@@ -87,11 +87,6 @@ __device__ __forceinline__ bool dw_wait(DwShared& sh, const DwArgs& a, uint64_t*
   return mbar_wait<false>(bar, parity, wc);
 }
 
-// generic-proxy writes to shared memory -> visible to the tensor cores' (async proxy) reads
-__device__ __forceinline__ void fence_proxy_async_shared() {
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
-
 template <int kHS>
 __global__ void __launch_bounds__(kDwThreads, 1)
     k_dw_stream(const __grid_constant__ CUtensorMap tm_p, const __grid_constant__ CUtensorMap tm_h, DwArgs a) {

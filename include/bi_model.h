@@ -101,6 +101,37 @@ BI_API bi_status bi_qk_norm_rope_bwd(const uint16_t* dq_out, const uint16_t* dk_
                                      int32_t R, uint16_t* dq, uint16_t* dk, int64_t dq_ld, int64_t dk_ld, float* dgq,
                                      float* dgk, int32_t* dev_status, void* ws, size_t ws_bytes, void* stream);
 
+/*
+ * Softmax attention over S sequences: out_i = sum_j p_ij v_j with p_i = softmax_j(scale q_i . k_j)
+ * over the keys that query i sees, and lse_i = log sum_j exp(scale q_i . k_j).
+ *   q [Tq][Hq][D], k, v [Tk][Hkv][D] bf16: heads are D apart, tokens q_ld, k_ld, v_ld elements
+ *     (slices of one projection's output, or caches); 16-byte aligned, strides multiples of 8.
+ *     Query head h reads key/value head h / (Hq / Hkv).
+ *   q_offsets, k_offsets [S + 1] int64 (device): sequence s has the query rows
+ *     q_offsets[s] .. q_offsets[s+1] - 1 and the key rows from k_offsets[s] on; k_lens [S] int32
+ *     (device) how many of the rows up to k_offsets[s+1] are keys (a cache with room behind them),
+ *     NULL for all.  For packed self-attention pass the same offsets twice.
+ *   causal != 0: the queries are the last ones of their sequence's positions: query i of n sees the keys
+ *     j <= i + (keys - n).  A decode step is one query a sequence over its cache.
+ *   out [Tq][Hq][D] bf16, lse [Hq][Tq] float.  A query that sees no key gets zeros and -infinity.  Rows
+ *     in no sequence are left as they were; key rows in none are not used, whatever they hold.
+ *   scale > 0, finite;  D 64 or 128;  Hq a multiple of Hkv, Hq / Hkv <= 128, Hkv <= 4096;
+ *   0 <= S;  0 <= Tq, Tk < 2^31 - 512
+ * A row's result has the same bits in any batch and whether it is computed among its sequence's other
+ * queries (prefill) or alone over a cache (decode).  A NaN or infinity in a key or value row of a sequence
+ * reaches every query of that sequence that shares a 128-row tile with one that sees it.
+ * The terms of the softmax are rounded to bf16 for the product with v; sums, maxima and lse are fp32.
+ * Device status: BI_ERR_BAD_OFFSETS (offsets that decrease or leave the tensors, k_lens below 0 or past the
+ * next offset): nothing is written then.  Returns BI_ERR_WORKSPACE for a ws below
+ * bi_attn_fwd_workspace_bytes(...) bytes or not 256-byte aligned, and the codes of the entry points above.
+ */
+BI_API size_t bi_attn_fwd_workspace_bytes(int64_t Tq, int64_t Tk, int32_t S, int32_t Hq, int32_t Hkv, int32_t D);
+BI_API bi_status bi_attn_fwd(const uint16_t* q, const uint16_t* k, const uint16_t* v, int64_t q_ld, int64_t k_ld,
+                             int64_t v_ld, const int64_t* q_offsets, const int64_t* k_offsets, const int32_t* k_lens,
+                             int32_t S, int64_t Tq, int64_t Tk, int32_t Hq, int32_t Hkv, int32_t D, int32_t causal,
+                             float scale, uint16_t* out, float* lse, int32_t* dev_status, void* ws, size_t ws_bytes,
+                             void* stream);
+
 #ifdef __cplusplus
 }
 #endif
