@@ -8,5 +8,5 @@ package only loads it and marshals tensors.
 from .api import (BiError, LossOutputs, check_status, d3_stats, decode_d3, debug_force_timeout_once,  # noqa: F401
                   gemm_bf16, is_loss_fwd_bwd, logprob_fwd, make_workspace, profile_enable, profile_read,
                   profile_reset, rmsnorm, workspace_bytes)
-from .attention import attn_fwd, qk_norm_rope, qk_norm_rope_bwd  # noqa: F401
+from .attention import attn_bwd, attn_fwd, qk_norm_rope, qk_norm_rope_bwd  # noqa: F401
 from .optim import AdamWState, adamw_step  # noqa: F401

@@ -185,3 +185,40 @@ def attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_offsets: torch
                                _ptr(st), _ptr(ws), ws.numel(), _stream(dev))
     _raise_host(code, "bi_attn_fwd")
     return out, lse, st
+
+
+def attn_bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor,
+             lse: torch.Tensor, q_offsets: torch.Tensor, k_offsets: Optional[torch.Tensor] = None,
+             k_lens: Optional[torch.Tensor] = None, causal: bool = True, scale: Optional[float] = None,
+             ws: Optional[torch.Tensor] = None, dq: Optional[torch.Tensor] = None, dk: Optional[torch.Tensor] = None,
+             dv: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None):
+    """The gradient of ``attn_fwd`` for dout [Tq, Hq, D], from its inputs and its results ``out`` and
+    ``lse``.  dq, dk and dv may be slices of one buffer; rows in no sequence are left as they were.
+    Returns (dq [Tq, Hq, D], dk, dv [Tk, Hkv, D] bf16, status)."""
+    dev = q.device
+    S, scale, k_offsets, q_ld, k_ld, v_ld = _attn_common(q, k, v, q_offsets, k_offsets, k_lens, scale, dev)
+    Tq, Hq, D = q.shape
+    Tk, Hkv = k.shape[0], k.shape[1]
+    do_ld = _rows(dout, "dout", dev, q.shape)
+    _need(out, "out", torch.bfloat16, dev, q.shape)
+    _need(lse, "lse", torch.float32, dev, (Hq, Tq))
+    lib = _lib.load()
+    if ws is None:
+        ws = torch.empty(max(lib.bi_attn_bwd_workspace_bytes(Tq, Tk, S, Hq, Hkv, D), 256), dtype=torch.uint8, device=dev)
+    else:
+        _need(ws, "ws", torch.uint8, dev)
+    if dq is None:
+        dq = torch.empty(Tq, Hq, D, dtype=torch.bfloat16, device=dev)
+    if dk is None:
+        dk = torch.empty(Tk, Hkv, D, dtype=torch.bfloat16, device=dev)
+    if dv is None:
+        dv = torch.empty(Tk, Hkv, D, dtype=torch.bfloat16, device=dev)
+    dq_ld, dk_ld, dv_ld = (_rows(dq, "dq", dev, q.shape), _rows(dk, "dk", dev, k.shape), _rows(dv, "dv", dev, k.shape))
+    st = _status(status, dev)
+    with _on(dev):
+        code = lib.bi_attn_bwd(_ptr(dout), do_ld, _ptr(q), _ptr(k), _ptr(v), q_ld, k_ld, v_ld, _ptr(out), _ptr(lse),
+                               _ptr(q_offsets), _ptr(k_offsets), _ptr(k_lens), S, Tq, Tk, Hq, Hkv, D,
+                               1 if causal else 0, scale, _ptr(dq), _ptr(dk), _ptr(dv), dq_ld, dk_ld, dv_ld, _ptr(st),
+                               _ptr(ws), ws.numel(), _stream(dev))
+    _raise_host(code, "bi_attn_bwd")
+    return dq, dk, dv, st

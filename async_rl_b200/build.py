@@ -17,7 +17,8 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libbi_isloss.so")
 SOURCES = ["bi_api.cu", "bi_rope.cu", "bi_adamw.cu", "bi_attn.cu"]
 HEADERS = ["host.h", "sm100.cuh", "kernels_lm.cuh", "kernels_decode.cuh", "kernels_dw.cuh", "kernels_model.cuh",
-           "kernels_small.cuh", "kernels_rope.cuh", "kernels_adamw.cuh", "kernels_attn.cuh"]
+           "kernels_small.cuh", "kernels_rope.cuh", "kernels_adamw.cuh", "kernels_attn.cuh",
+           "kernels_attn_bwd.cuh"]
 PUBLIC = ["bi_isloss.h", "bi_model.h", "bi_optim.h"]
 
 

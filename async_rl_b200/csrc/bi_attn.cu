@@ -3,7 +3,7 @@
 
 #include "bi_model.h"
 #include "host.h"
-#include "kernels_attn.cuh"
+#include "kernels_attn_bwd.cuh"
 
 namespace {
 
@@ -67,6 +67,31 @@ FwdLayout fwd_layout(const Shape& z) {
   return L;
 }
 
+struct BwdLayout {
+  size_t head, seqs, units, seqs_kv, units_kv, st, total;
+  int32_t cap_q, cap_kv;
+};
+BwdLayout bwd_layout(const Shape& z) {
+  BwdLayout L{};
+  const int64_t S = z.S > 0 ? z.S : 1;
+  L.cap_q = static_cast<int32_t>(S + z.Tq / z.tpt + 1);
+  L.cap_kv = static_cast<int32_t>(S + z.Tk / bi::kAtTile + 1);
+  size_t o = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = o;
+    o = align_up(o + bytes, 256);
+    return at;
+  };
+  L.head = take(2 * sizeof(bi::AttnPlanHead));
+  L.seqs = take(static_cast<size_t>(S) * sizeof(bi::AttnSeq));
+  L.units = take(static_cast<size_t>(L.cap_q) * sizeof(bi::AttnUnit));
+  L.seqs_kv = take(static_cast<size_t>(S) * sizeof(bi::AttnSeq));
+  L.units_kv = take(static_cast<size_t>(L.cap_kv) * sizeof(bi::AttnUnit));
+  L.st = take(static_cast<size_t>(z.Hkv) * L.cap_q * 2 * bi::kAtTile * 4);
+  L.total = o;
+  return L;
+}
+
 // [T][heads][D] bf16 with `ld` elements between tokens, box {64 columns, box_heads, box_rows}.
 bool make_map_heads(CUtensorMap* m, const void* base, int64_t T, int32_t heads, int32_t D, int64_t ld, int box_heads,
                     int box_rows) {
@@ -91,7 +116,14 @@ int attn_device() {
   if (sms <= 0 || sms > kMaxSms || cudaGetDevice(&dev) != cudaSuccess) return 0;
   std::lock_guard<std::mutex> lk(mu);
   if (!ready[dev]) {
-    if (cudaFuncSetAttribute(bi::k_attn_fwd<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    const int bwd128 = bi::AtBwdTile<128>::smem + bi::kAtBwdSharedBytes;
+    const int bwd64 = bi::AtBwdTile<64>::smem + bi::kAtBwdSharedBytes;
+    constexpr auto kSmem = cudaFuncAttributeMaxDynamicSharedMemorySize;
+    if (cudaFuncSetAttribute(bi::k_attn_dkv<128>, kSmem, bwd128) != cudaSuccess ||
+        cudaFuncSetAttribute(bi::k_attn_dkv<64>, kSmem, bwd64) != cudaSuccess ||
+        cudaFuncSetAttribute(bi::k_attn_dq<128>, kSmem, bwd128) != cudaSuccess ||
+        cudaFuncSetAttribute(bi::k_attn_dq<64>, kSmem, bwd64) != cudaSuccess ||
+        cudaFuncSetAttribute(bi::k_attn_fwd<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              bi::AtFwdTile<128>::smem + bi::kAtSharedBytes) != cudaSuccess ||
         cudaFuncSetAttribute(bi::k_attn_fwd<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              bi::AtFwdTile<64>::smem + bi::kAtSharedBytes) != cudaSuccess)
@@ -113,6 +145,29 @@ bool launch_fwd(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap&
     const int64_t cap = static_cast<int64_t>(sms) * 16;
     ProfScope ps(kKAttnJoin, s);
     bi::k_attn_join<D><<<static_cast<unsigned>(want < cap ? want : cap), bi::kAtJoinThreads, 0, s>>>(a, S);
+  }
+  return cudaGetLastError() == cudaSuccess;
+}
+
+template <int D>
+bool launch_bwd(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mdo,
+                const bi::AttnBwdArgs& dq, const bi::AttnBwdArgs& dkv, const BwdLayout& L, int sms, cudaStream_t s) {
+  const auto grid = [&](int64_t units, int per_sm) {
+    const int64_t n = units * dq.Hkv, cap = static_cast<int64_t>(sms) * per_sm;
+    return static_cast<unsigned>(n < cap ? n : cap);
+  };
+  constexpr int smem = bi::AtBwdTile<D>::smem + bi::kAtBwdSharedBytes;
+  {
+    ProfScope ps(kKAttnPre, s);
+    bi::k_attn_pre<D><<<grid(L.cap_q, 8), bi::kAtPreThreads, 0, s>>>(dq);
+  }
+  {
+    ProfScope ps(kKAttnDkv, s);
+    bi::k_attn_dkv<D><<<grid(L.cap_kv, 1), bi::kAtBwdThreads, smem, s>>>(mq, mk, mv, mdo, dkv);
+  }
+  {
+    ProfScope ps(kKAttnDq, s);
+    bi::k_attn_dq<D><<<grid(L.cap_q, 1), bi::kAtBwdThreads, smem, s>>>(mq, mk, mv, mdo, dq);
   }
   return cudaGetLastError() == cudaSuccess;
 }
@@ -197,6 +252,111 @@ bi_status bi_attn_fwd(const uint16_t* q, const uint16_t* k, const uint16_t* v, i
   const unsigned grid = static_cast<unsigned>(most < sms ? most : sms);
   const bool ok = D == 128 ? launch_fwd<128>(mq, mk, mv, a, grid, L.cap_part > 0, S, sms, s)
                            : launch_fwd<64>(mq, mk, mv, a, grid, L.cap_part > 0, S, sms, s);
+  return ok ? BI_OK : BI_ERR_CUDA;
+}
+
+size_t bi_attn_bwd_workspace_bytes(int64_t Tq, int64_t Tk, int32_t S, int32_t Hq, int32_t Hkv, int32_t D) {
+  Shape z{Tq, Tk, S, Hq, Hkv, D, 0, 0};
+  if (!sizes_ok(z) || !shape_ok(z)) return 0;
+  return bwd_layout(z).total;
+}
+
+bi_status bi_attn_bwd(const uint16_t* dout, int64_t dout_ld, const uint16_t* q, const uint16_t* k, const uint16_t* v,
+                      int64_t q_ld, int64_t k_ld, int64_t v_ld, const uint16_t* out, const float* lse,
+                      const int64_t* q_offsets, const int64_t* k_offsets, const int32_t* k_lens, int32_t S, int64_t Tq,
+                      int64_t Tk, int32_t Hq, int32_t Hkv, int32_t D, int32_t causal, float scale, uint16_t* dq,
+                      uint16_t* dk, uint16_t* dv, int64_t dq_ld, int64_t dk_ld, int64_t dv_ld, int32_t* dev_status,
+                      void* ws, size_t ws_bytes, void* stream) {
+  Shape z{Tq, Tk, S, Hq, Hkv, D, 0, 0};
+  if (!dev_status || !sizes_ok(z) || !(scale > 0.f) || !std::isfinite(scale)) return BI_ERR_INVALID_ARG;
+  if (!shape_ok(z)) return BI_ERR_UNSUPPORTED_SHAPE;
+  if (S > 0 && (!q_offsets || !k_offsets)) return BI_ERR_INVALID_ARG;
+  if (Tq > 0 && (!rows_ok(q, q_ld, Hq, D) || !rows_ok(dout, dout_ld, Hq, D) || !rows_ok(dq, dq_ld, Hq, D) || !out ||
+                 !aligned16(out) || !lse || dq == q || dq == dout || dq == out))
+    return BI_ERR_INVALID_ARG;
+  if (Tk > 0 && (!rows_ok(k, k_ld, Hkv, D) || !rows_ok(v, v_ld, Hkv, D) || !rows_ok(dk, dk_ld, Hkv, D) ||
+                 !rows_ok(dv, dv_ld, Hkv, D) || dk == k || dk == v || dv == k || dv == v || dk == dv || dk == dq || dv == dq))
+    return BI_ERR_INVALID_ARG;
+  const BwdLayout L = bwd_layout(z);
+  if (!ws || ws_bytes < L.total || (reinterpret_cast<uintptr_t>(ws) & 255u)) return BI_ERR_WORKSPACE;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (S == 0 || (Tq == 0 && Tk == 0))
+    return cudaMemsetAsync(dev_status, 0, sizeof(int32_t), s) == cudaSuccess ? BI_OK : BI_ERR_CUDA;
+  const int sms = attn_device();
+  if (sms <= 0) return BI_ERR_CUDA;
+  uint8_t* w8 = static_cast<uint8_t*>(ws);
+  bi::AttnPlanArgs p{};
+  p.qo = q_offsets;
+  p.ko = k_offsets;
+  p.kl = k_lens;
+  p.Tq = Tq;
+  p.Tk = Tk;
+  p.S = S;
+  p.mode = bi::kPlanDq;
+  p.causal = causal != 0;
+  p.step = z.tpt;
+  p.tpt = z.tpt;
+  p.sms = sms;
+  p.Hkv = Hkv;
+  p.cap_units = L.cap_q;
+  p.seqs = reinterpret_cast<bi::AttnSeq*>(w8 + L.seqs);
+  p.units = reinterpret_cast<bi::AttnUnit*>(w8 + L.units);
+  p.head = reinterpret_cast<bi::AttnPlanHead*>(w8 + L.head);
+  p.status = dev_status;
+  bi::AttnPlanArgs pk = p;
+  pk.mode = bi::kPlanDkv;
+  pk.step = bi::kAtTile;
+  pk.cap_units = L.cap_kv;
+  pk.seqs = reinterpret_cast<bi::AttnSeq*>(w8 + L.seqs_kv);
+  pk.units = reinterpret_cast<bi::AttnUnit*>(w8 + L.units_kv);
+  pk.head = p.head + 1;
+  pk.status = nullptr;
+  // a call without queries or keys reads none of them: any address serves the maps
+  CUtensorMap mq, mk, mv, mdo;
+  const auto map = [&](CUtensorMap* m, const void* at, int64_t T, int32_t heads, int64_t ld, int bh, int br) {
+    return T > 0 ? make_map_heads(m, at, T, heads, D, ld, bh, br)
+                 : make_map_heads(m, ws, 0, heads, D, static_cast<int64_t>(heads) * D, bh, br);
+  };
+  if (!map(&mq, q, Tq, Hq, q_ld, z.G, z.tpt) || !map(&mdo, dout, Tq, Hq, dout_ld, z.G, z.tpt) ||
+      !map(&mk, k, Tk, Hkv, k_ld, 1, bi::kAtTile) || !map(&mv, v, Tk, Hkv, v_ld, 1, bi::kAtTile))
+    return BI_ERR_CUDA;
+  {
+    ProfScope ps(kKAttnPlan, s);
+    bi::k_attn_plan<<<2, bi::kPlanThreads, 0, s>>>(p, pk);
+  }
+  bi::AttnBwdArgs a{};
+  a.seqs = p.seqs;
+  a.units = p.units;
+  a.head = p.head;
+  a.rows = p.seqs;
+  a.st = reinterpret_cast<float*>(w8 + L.st);
+  a.tiles = L.cap_q;
+  a.out = out;
+  a.dout = dout;
+  a.lse = lse;
+  a.do_ld = dout_ld;
+  a.Tq = Tq;
+  a.o0 = dq;
+  a.ld0 = dq_ld;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.G = z.G;
+  a.tpt = z.tpt;
+  a.causal = p.causal;
+  a.c = scale * bi::kLog2e;
+  a.scale = scale;
+  a.status = dev_status;
+  a.limit_ns = kWaitLimitNs;
+  bi::AttnBwdArgs b = a;
+  b.seqs = pk.seqs;
+  b.units = pk.units;
+  b.head = pk.head;
+  b.o0 = dk;
+  b.o1 = dv;
+  b.ld0 = dk_ld;
+  b.ld1 = dv_ld;
+  const bool ok = D == 128 ? launch_bwd<128>(mq, mk, mv, mdo, a, b, L, sms, s)
+                           : launch_bwd<64>(mq, mk, mv, mdo, a, b, L, sms, s);
   return ok ? BI_OK : BI_ERR_CUDA;
 }
 

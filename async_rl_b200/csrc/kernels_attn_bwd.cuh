@@ -1,0 +1,769 @@
+// kernels_attn_bwd.cuh -- the gradient of softmax attention (kernels_attn.cuh has the forward).
+//
+// Mathematics.  With p_ij = exp(scale q_i . k_j - lse_i) on the visible pairs and the row's number
+// delta_i = do_i . out_i:
+//   dv_j = sum_i p_ij do_i,   ds_ij = p_ij (do_i . v_j - delta_i),
+//   dk_j = scale sum_i ds_ij q_i,   dq_i = scale sum_j ds_ij k_j.
+// p is recomputed from lse, so nothing of size queries x keys is ever stored.
+//
+// Two kernels.  k_attn_dkv holds 128 keys of one key/value head and runs over the query tiles that
+// see them (4 products a tile pair); k_attn_dq holds 128 query rows and runs over the key tiles that
+// they see (3 products).  One kernel for all three gradients needs 5 products, not 7, but has to add
+// dQ up over CTAs: with atomics the order, and so the bits, would change from run to run, and 64 KB
+// of fp32 additions a tile pair would go to L2.  Here every sum has a fixed order that depends on the
+// places in the sequence only, so a sequence's gradients have the same bits in any batch.
+//
+// Both are bound by the tensor cores, with the exponentials (16 a clock and SM) next: 2048 and 1536
+// clocks of products (D = 128) against 1024 of exponentials a pair of tiles.
+//
+// Rows behave as in the forward: a tile of 128 rows is floor(128 / G) tokens times the G heads that
+// share a key/value head, so the gradients of shared heads are added up in the accumulators.
+#pragma once
+
+#include "kernels_attn.cuh"
+
+namespace bi {
+
+struct AttnBwdArgs {
+  const AttnSeq* seqs;         // of this kernel's plan
+  const AttnUnit* units;
+  const AttnPlanHead* head;
+  const AttnSeq* rows;         // of the dQ plan: unit0 counts its row tiles
+  float* st;                   // [Hkv][tiles][2][128]: -lse log2(e) and -delta of each row of a tile
+  int64_t tiles;
+  const uint16_t *out, *dout;  // k_attn_pre
+  const float* lse;
+  int64_t do_ld, Tq;
+  uint16_t *o0, *o1;           // dK and dV, or dQ
+  int64_t ld0, ld1;
+  int32_t Hq, Hkv, G, tpt;
+  int32_t causal;
+  float c;                     // scale log2(e)
+  float scale;
+  int32_t* status;
+  uint64_t limit_ns;
+};
+
+// ----------------------------------------------------------------------------------------------
+// rows' numbers
+// ----------------------------------------------------------------------------------------------
+// Bound by HBM (4 bytes an element of out).  A row of D values takes D / 8 lanes.  Rows of the tile
+// that hold no query get -lse = -inf, which makes every p of theirs 0.
+constexpr int kAtPreThreads = 256;
+template <int D>
+__global__ void __launch_bounds__(kAtPreThreads) k_attn_pre(const AttnBwdArgs a) {
+  constexpr int L = D / 8;                    // lanes of a row
+  constexpr int R = kAtPreThreads / L;        // rows at a time
+  const int sub = threadIdx.x / L, lane = threadIdx.x % L;
+  const int64_t n = static_cast<int64_t>(a.head->nunits) * a.Hkv;
+  for (int64_t u = blockIdx.x; u < n; u += gridDim.x) {
+    const AttnUnit w = a.units[u / a.Hkv];
+    const int32_t h = static_cast<int32_t>(u % a.Hkv);
+    const AttnSeq q = a.seqs[w.seq];
+    float* st = a.st + (h * a.tiles + q.unit0 + w.t0 / a.tpt) * (2 * kAtTile);
+#pragma unroll
+    for (int r0 = 0; r0 < kAtTile; r0 += R) {
+      const int r = r0 + sub;
+      const int tok_in = r / a.G, g = r - tok_in * a.G;
+      const bool valid = tok_in < a.tpt && w.t0 + tok_in < q.lq;
+      const int64_t t = q.q0 + w.t0 + tok_in;
+      const int32_t head = h * a.G + g;
+      float sum = 0.f;
+      if (valid) {
+        const uint4 x = *reinterpret_cast<const uint4*>(a.out + (t * a.Hq + head) * D + lane * 8);
+        const uint4 y = *reinterpret_cast<const uint4*>(a.dout + t * a.do_ld + head * D + lane * 8);
+        const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          sum = fmaf(__uint_as_float(xs[e] << 16), __uint_as_float(ys[e] << 16), sum);
+          sum = fmaf(__uint_as_float(xs[e] & 0xffff0000u), __uint_as_float(ys[e] & 0xffff0000u), sum);
+        }
+      }
+#pragma unroll
+      for (int o = L / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if (lane == 0) {
+        const float lse = valid ? a.lse[static_cast<int64_t>(head) * a.Tq + t] : -INFINITY;
+        st[r] = lse == -INFINITY ? -INFINITY : -lse * kLog2e;  // a row that sees nothing has no p
+        st[kAtTile + r] = -sum;
+      }
+    }
+  }
+}
+
+// ----------------------------------------------------------------------------------------------
+// shared by both kernels
+// ----------------------------------------------------------------------------------------------
+constexpr int kAtBwdThreads = 320;  // warps 0-7: p and ds; 8: TMA; 9: MMA
+constexpr int kAtSlotsA = 3, kAtSlotsB = 2;
+
+template <int D>
+struct AtBwdTile {
+  static constexpr int tile_bytes = kAtTile * D * 2;
+  static constexpr int ring_a = 2 * tile_bytes;                        // behind the two held tiles
+  static constexpr int ring_b = ring_a + kAtSlotsA * tile_bytes;
+  static constexpr int smem = ring_b + kAtSlotsB * tile_bytes;
+};
+struct AtBwdShared {
+  float st[2][2][kAtTile];
+  uint64_t held_full, held_empty;
+  uint64_t a_full[kAtSlotsA], a_empty[kAtSlotsA];
+  uint64_t b_full[kAtSlotsB], b_empty[kAtSlotsB];
+  uint64_t st_full[2], st_empty[2];
+  uint64_t s_full[2], dp_full;
+  uint64_t p_full[2], ds_full[2];  // halves of the columns (dQ: ds_full[0] for both)
+  uint64_t acc_full, done;
+  uint32_t tmem_base;
+  volatile uint32_t abort_flag;
+};
+constexpr int kAtBwdSharedBytes = static_cast<int>((sizeof(AtBwdShared) + 127) / 128 * 128);
+
+// A ring's slot and its phase.
+template <int N>
+struct AtRing {
+  uint32_t slot = 0, phase = 0;
+  __device__ __forceinline__ void next() { ring_advance(slot, phase, N); }
+};
+
+// Warp roles' common start and end; returns the base of tensor memory.
+__device__ __forceinline__ uint32_t at_bwd_begin(AtBwdShared& sh) {
+  if (threadIdx.x == 0) {
+    mbar_init(&sh.held_full, 1);
+    mbar_init(&sh.held_empty, 1);
+    for (int i = 0; i < kAtSlotsA; ++i) {
+      mbar_init(&sh.a_full[i], 1);
+      mbar_init(&sh.a_empty[i], 1);
+    }
+    for (int i = 0; i < kAtSlotsB; ++i) {
+      mbar_init(&sh.b_full[i], 1);
+      mbar_init(&sh.b_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.st_full[i], 1);
+      mbar_init(&sh.st_empty[i], 1);
+      mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.p_full[i], 256);
+      mbar_init(&sh.ds_full[i], 256);
+    }
+    mbar_init(&sh.dp_full, 1);
+    mbar_init(&sh.acc_full, 1);
+    mbar_init(&sh.done, 1);
+    sh.abort_flag = 0u;
+    fence_mbar_init_cluster();
+  }
+  if (threadIdx.x / 32 == 9) {
+    tmem_alloc(&sh.tmem_base, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  return sh.tmem_base;
+}
+__device__ __forceinline__ void at_bwd_end(AtBwdShared& sh, uint32_t tmem) {
+  tc_fence_before();
+  __syncthreads();
+  if (sh.abort_flag != 0u) {  // on the error path a copy or a commit may still be in flight
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 50000u) {
+    }
+  }
+  if (threadIdx.x / 32 == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// D[128 x 128] = A[128 x Dh] B[128 x Dh]^T, both K-major tiles in shared memory (one thread).
+template <int D>
+__device__ __forceinline__ void at_mma_ss(uint32_t d, uint64_t da, uint64_t db) {
+  constexpr uint32_t idesc = idesc_bf16(128, 128, false, false);
+  constexpr uint64_t blk = kAUnitBytes >> 4;
+#pragma unroll
+  for (int b = 0; b < D / 64; ++b)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) umma_bf16(d, da + b * blk + 2 * k, db + b * blk + 2 * k, idesc, (b | k) ? 1u : 0u);
+}
+// Half of D[128 x Dh] += A[128 x 128] B[128 x Dh]: A in tensor memory as at_put leaves it, B a tile
+// read along its rows (one thread).
+template <int D>
+__device__ __forceinline__ void at_mma_ts(uint32_t d, uint32_t a, uint64_t db, int half, bool first) {
+  constexpr uint32_t idesc = idesc_bf16(128, D, false, true);
+#pragma unroll
+  for (int k = 4 * half; k < 4 * half + 4; ++k)
+    umma_bf16_ta(d, a + (k / 2) * 32 + (k % 2) * 8, db + k * (2048 >> 4), idesc, (k > 0 || !first) ? 1u : 0u);
+}
+
+// A thread's columns of a 128-column tile: 32 of each half, [half * 64 + X * 32, +32), X its group.
+// Its bf16 results go into the first 16 of the 32 columns that it read.
+__device__ __forceinline__ void at_get(uint32_t t, uint32_t (&s)[2][32]) {
+  tmem_ld32(t, s[0]);
+  tmem_ld32(t + 64, s[1]);
+  tmem_ld_wait();
+  tmem_ld_pin(s[0]);
+  tmem_ld_pin(s[1]);
+}
+__device__ __forceinline__ void at_put(uint32_t t, const float2 (&p)[16]) {
+  uint32_t w[16];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) w[e] = pack_bf16x2(p[e].x, p[e].y);  // bf16: what the tensor cores take
+  tmem_st16(t, w);
+}
+// 32 columns of an accumulator, scaled, as bf16 (whole warp; stored where `valid`).
+__device__ __forceinline__ void at_store32(uint32_t t, float scale, uint16_t* o, bool valid) {
+  uint32_t s[32], w[16];
+  tmem_ld32(t, s);
+  tmem_ld_wait();
+  tmem_ld_pin(s);
+#pragma unroll
+  for (int e = 0; e < 16; ++e)
+    w[e] = pack_bf16x2(__uint_as_float(s[2 * e]) * scale, __uint_as_float(s[2 * e + 1]) * scale);
+  if (valid)
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      reinterpret_cast<uint4*>(o)[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+}
+__device__ __forceinline__ void at_zero32(uint16_t* o) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) reinterpret_cast<uint4*>(o)[e] = make_uint4(0u, 0u, 0u, 0u);
+}
+__device__ __forceinline__ float2 at_pair(const uint32_t (&s)[32], int e) {
+  return make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));
+}
+
+// ----------------------------------------------------------------------------------------------
+// dK, dV: keys are the lanes, query rows the columns
+// ----------------------------------------------------------------------------------------------
+// Tensor memory: S^T, dP^T, dV, dK.  P^T and dS^T replace the scores that they come from and are the
+// A operands of dV and dK.  The issue order makes two phases: while the tensor cores work on
+// dV += P_i dO_i and S_{i+1}, ds_i is computed; while they work on dK += dS_i Q_i and dP_{i+1},
+// p_{i+1} is.
+struct AtKvUnit {
+  AttnSeq q;
+  int32_t h, t0;
+  int32_t i0, i1;   // query tiles that see a key of the unit
+  int64_t tile0;    // of the sequence's first query tile
+};
+__device__ __forceinline__ AtKvUnit at_kv_unit(const AttnBwdArgs& a, int64_t u) {
+  AtKvUnit x;
+  const AttnUnit w = a.units[u / a.Hkv];
+  x.h = static_cast<int32_t>(u % a.Hkv);
+  x.q = a.seqs[w.seq];
+  x.t0 = w.t0;
+  const int32_t first = attn_first_query(w.t0, x.q.lq, x.q.lk, a.causal);
+  x.i1 = (x.q.lq + a.tpt - 1) / a.tpt;
+  x.i0 = first >= x.q.lq ? x.i1 : first / a.tpt;
+  x.tile0 = a.rows[w.seq].unit0;
+  return x;
+}
+
+template <int D>
+__device__ __forceinline__ void at_dkv_load(AtBwdShared& sh, const AttnBwdArgs& a, uint32_t smem, int64_t nu,
+                                            const CUtensorMap* mq, const CUtensorMap* mk, const CUtensorMap* mv,
+                                            const CUtensorMap* mdo) {
+  using T = AtBwdTile<D>;
+  const WaitCtl wc{&sh.abort_flag, a.status, a.limit_ns};
+  tma_prefetch_desc(mq);
+  tma_prefetch_desc(mk);
+  tma_prefetch_desc(mv);
+  tma_prefetch_desc(mdo);
+  const uint32_t bytes = static_cast<uint32_t>(a.tpt * a.G) * 128u * (D / 64);
+  AtRing<kAtSlotsA> ra;
+  AtRing<kAtSlotsB> rb;
+  AtRing<2> rs;
+  uint32_t hph = 0;
+  for (int64_t u = blockIdx.x; u < nu; u += gridDim.x) {
+    const AtKvUnit x = at_kv_unit(a, u);
+    if (x.i0 >= x.i1) continue;
+    if (!mbar_wait<false>(&sh.held_empty, hph ^ 1u, wc)) return;
+    hph ^= 1u;
+    mbar_arrive_expect_tx(&sh.held_full, 2 * T::tile_bytes);
+    const int32_t key = static_cast<int32_t>(x.q.k0) + x.t0;
+#pragma unroll
+    for (int b = 0; b < D / 64; ++b) {
+      tma_load_3d(smem + b * kAUnitBytes, mk, &sh.held_full, b * 64, x.h, key);
+      tma_load_3d(smem + T::tile_bytes + b * kAUnitBytes, mv, &sh.held_full, b * 64, x.h, key);
+    }
+    const float* st = a.st + (x.h * a.tiles + x.tile0) * (2 * kAtTile);
+    for (int32_t i = x.i0; i < x.i1; ++i) {
+      const int32_t row = static_cast<int32_t>(x.q.q0) + i * a.tpt;
+      if (!mbar_wait<false>(&sh.a_empty[ra.slot], ra.phase ^ 1u, wc)) return;
+      mbar_arrive_expect_tx(&sh.a_full[ra.slot], bytes);
+#pragma unroll
+      for (int b = 0; b < D / 64; ++b)
+        tma_load_3d(smem + T::ring_a + ra.slot * T::tile_bytes + b * kAUnitBytes, mq, &sh.a_full[ra.slot], b * 64,
+                    x.h * a.G, row);
+      ra.next();
+      if (!mbar_wait<false>(&sh.st_empty[rs.slot], rs.phase ^ 1u, wc)) return;
+      mbar_arrive_expect_tx(&sh.st_full[rs.slot], 2 * kAtTile * 4);
+      bulk_load(smem_u32(&sh.st[rs.slot][0][0]), st + static_cast<int64_t>(i) * (2 * kAtTile), 2 * kAtTile * 4,
+                &sh.st_full[rs.slot]);
+      rs.next();
+      if (!mbar_wait<false>(&sh.b_empty[rb.slot], rb.phase ^ 1u, wc)) return;
+      mbar_arrive_expect_tx(&sh.b_full[rb.slot], bytes);
+#pragma unroll
+      for (int b = 0; b < D / 64; ++b)
+        tma_load_3d(smem + T::ring_b + rb.slot * T::tile_bytes + b * kAUnitBytes, mdo, &sh.b_full[rb.slot], b * 64,
+                    x.h * a.G, row);
+      rb.next();
+    }
+  }
+}
+
+template <int D>
+__device__ __forceinline__ void at_dkv_mma(AtBwdShared& sh, const AttnBwdArgs& a, uint8_t* smem_p, int64_t nu,
+                                           uint32_t tmem) {
+  using T = AtBwdTile<D>;
+  const WaitCtl wc{&sh.abort_flag, a.status, a.limit_ns};
+  const uint32_t smem = smem_u32(smem_p);
+  const int lane = threadIdx.x & 31;
+  constexpr uint32_t ts = T::tile_bytes >> 4;
+  const uint64_t dk = sdesc_k_sw128(smem), dv = sdesc_k_sw128(smem + T::tile_bytes);
+  const uint64_t dq_k = sdesc_k_sw128(smem + T::ring_a), dq_mn = sdesc_mn_sw128(smem + T::ring_a, kAUnitBytes);
+  const uint64_t do_k = sdesc_k_sw128(smem + T::ring_b), do_mn = sdesc_mn_sw128(smem + T::ring_b, kAUnitBytes);
+  const uint32_t t_s = tmem, t_dp = tmem + 128, t_dv = tmem + 256, t_dk = tmem + 256 + D;
+  AtRing<kAtSlotsA> ra, ra2;  // next tile to arrive, tile whose dK is next
+  AtRing<kAtSlotsB> rb, rb2;
+  AtRing<2> rs;
+  uint32_t hph = 0, ph = 0;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    const bool ok = __all_sync(0xffffffffu, mbar_wait<false>(bar, parity, wc));
+    tc_fence_after();
+    return ok;
+  };
+  for (int64_t u = blockIdx.x; u < nu; u += gridDim.x) {
+    const AtKvUnit x = at_kv_unit(a, u);
+    if (x.i0 >= x.i1) continue;
+    // rows behind the sequence's last query may be another sequence's, or hold anything: zeros
+    const int last_rows = (x.q.lq - (x.i1 - 1) * a.tpt) * a.G;
+    auto scores = [&](int32_t i) {
+      if (!wait(&sh.a_full[ra.slot], ra.phase)) return false;
+      if (i + 1 == x.i1) at_zero_rows<D>(smem_p + T::ring_a + ra.slot * T::tile_bytes, last_rows);
+      if (lane == 0) {
+        at_mma_ss<D>(t_s, dk, dq_k + ra.slot * ts);
+        umma_commit(&sh.s_full[0]);
+      }
+      ra.next();
+      return true;
+    };
+    auto dprobs = [&](int32_t i) {
+      if (!wait(&sh.b_full[rb.slot], rb.phase)) return false;
+      if (i + 1 == x.i1) at_zero_rows<D>(smem_p + T::ring_b + rb.slot * T::tile_bytes, last_rows);
+      if (lane == 0) {
+        at_mma_ss<D>(t_dp, dv, do_k + rb.slot * ts);
+        umma_commit(&sh.dp_full);
+        if (i + 1 == x.i1) umma_commit(&sh.held_empty);
+      }
+      rb.next();
+      return true;
+    };
+    if (!wait(&sh.held_full, hph)) break;
+    hph ^= 1u;
+    if (!scores(x.i0) || !dprobs(x.i0)) break;
+    bool ok = true;
+    for (int32_t i = x.i0; i < x.i1 && ok; ++i) {
+      const bool first = i == x.i0, next = i + 1 < x.i1;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        ok = ok && wait(&sh.p_full[half], ph);
+        if (ok && lane == 0) at_mma_ts<D>(t_dv, t_s, do_mn + rb2.slot * ts, half, first);
+      }
+      if (!ok) break;
+      if (lane == 0) umma_commit(&sh.b_empty[rb2.slot]);
+      rb2.next();
+      if (next && !scores(i + 1)) ok = false;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        ok = ok && wait(&sh.ds_full[half], ph);
+        if (ok && lane == 0) at_mma_ts<D>(t_dk, t_dp, dq_mn + ra2.slot * ts, half, first);
+      }
+      if (!ok) break;
+      if (lane == 0) {
+        umma_commit(&sh.a_empty[ra2.slot]);
+        umma_commit(&sh.st_empty[rs.slot]);
+        if (!next) umma_commit(&sh.acc_full);
+      }
+      ra2.next();
+      rs.next();
+      ph ^= 1u;
+      if (next && !dprobs(i + 1)) ok = false;
+    }
+    if (!ok) break;
+  }
+  __syncwarp();
+  if (lane == 0) umma_commit(&sh.done);
+  mbar_wait<false>(&sh.done, 0u, wc);
+}
+
+template <int D>
+__device__ __forceinline__ void at_dkv_probs(AtBwdShared& sh, const AttnBwdArgs& a, int64_t nu, uint32_t tmem) {
+  const WaitCtl wc{&sh.abort_flag, a.status, a.limit_ns};
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int X = warp >> 2, key_in = (warp & 3) * 32 + lane;
+  const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+  const uint32_t t_s = tmem + lanes + X * 32, t_dp = t_s + 128;
+  const uint32_t t_acc = tmem + lanes + 256 + (X == 0 ? D : 0);  // group 0 stores dK, group 1 dV
+  uint32_t ph = 0, aph = 0;
+  AtRing<2> rs;
+  const float2 cc = make_float2(a.c, a.c);
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    const bool ok = __all_sync(0xffffffffu, mbar_wait<false>(bar, parity, wc));
+    tc_fence_after();
+    return ok;
+  };
+  for (int64_t u = blockIdx.x; u < nu; u += gridDim.x) {
+    const AtKvUnit x = at_kv_unit(a, u);
+    const int32_t key = x.t0 + key_in;
+    const bool valid = key < x.q.lk;
+    uint16_t* o = X == 0 ? a.o0 + (x.q.k0 + key) * a.ld0 + x.h * D : a.o1 + (x.q.k0 + key) * a.ld1 + x.h * D;
+    if (x.i0 >= x.i1) {  // no query sees these keys
+      if (valid)
+#pragma unroll
+        for (int b = 0; b < D / 32; ++b) at_zero32(o + b * 32);
+      continue;
+    }
+    // this key's first query
+    const int32_t from = a.causal ? key - (x.q.lk - x.q.lq) : 0;
+    for (int32_t i = x.i0; i < x.i1; ++i) {
+      // columns below `low` do not see this key
+      const int64_t lw = (static_cast<int64_t>(from) - static_cast<int64_t>(i) * a.tpt) * a.G;
+      const int low = lw > kAtTile ? kAtTile : static_cast<int>(lw < 0 ? 0 : lw);
+      const bool masked = __any_sync(0xffffffffu, low > 0);
+      if (!wait(&sh.st_full[rs.slot], rs.phase)) return;
+      if (!wait(&sh.s_full[0], ph)) return;
+      const float4* nl = reinterpret_cast<const float4*>(&sh.st[rs.slot][0][X * 32]);
+      const float4* nd = reinterpret_cast<const float4*>(&sh.st[rs.slot][1][X * 32]);
+      uint32_t s[2][32];
+      float2 p[2][16];
+      at_get(t_s, s);
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        if (masked)
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (half * 64 + X * 32 + e < low) s[half][e] = 0xff800000u;  // -inf
+#pragma unroll
+        for (int e = 0; e < 16; e += 2) {
+          const float4 l = nl[half * 16 + e / 2];
+          const float2 y0 = fma2(at_pair(s[half], e), cc, make_float2(l.x, l.y));
+          const float2 y1 = fma2(at_pair(s[half], e + 1), cc, make_float2(l.z, l.w));
+          p[half][e] = make_float2(ex2_approx(y0.x), ex2_approx(y0.y));
+          p[half][e + 1] = make_float2(ex2_approx(y1.x), ex2_approx(y1.y));
+        }
+        at_put(t_s + half * 64, p[half]);
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&sh.p_full[half]);
+      }
+      if (!wait(&sh.dp_full, ph)) return;
+      at_get(t_dp, s);
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        if (masked)
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (half * 64 + X * 32 + e < low) s[half][e] = 0u;  // p is 0 there; what v holds does not matter
+#pragma unroll
+        for (int e = 0; e < 16; e += 2) {
+          const float4 d = nd[half * 16 + e / 2];
+          p[half][e] = mul2(p[half][e], add2(at_pair(s[half], e), make_float2(d.x, d.y)));
+          p[half][e + 1] = mul2(p[half][e + 1], add2(at_pair(s[half], e + 1), make_float2(d.z, d.w)));
+        }
+        at_put(t_dp + half * 64, p[half]);
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&sh.ds_full[half]);
+      }
+      rs.next();
+      ph ^= 1u;
+    }
+    if (!wait(&sh.acc_full, aph)) return;
+    aph ^= 1u;
+#pragma unroll 1
+    for (int b = 0; b < D / 32; ++b) at_store32(t_acc + b * 32, X == 0 ? a.scale : 1.f, o + b * 32, valid);
+  }
+}
+
+// Rows [tpt G, 128) of every query tile are never loaded: zeros from the start.
+template <int D>
+__device__ __forceinline__ void at_zero_tails(uint8_t* ring, int slots, int rows) {
+  for (int i = threadIdx.x; i < slots * (D / 64) * (kAtTile - rows) * 8; i += kAtBwdThreads) {
+    const int v = i & 7, rest = i >> 3;
+    const int r = rows + rest % (kAtTile - rows), blk = rest / (kAtTile - rows);
+    *reinterpret_cast<uint4*>(ring + blk * kAUnitBytes + r * 128 + v * 16) = make_uint4(0u, 0u, 0u, 0u);
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kAtBwdThreads, 1)
+    k_attn_dkv(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+               const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mdo, const AttnBwdArgs a) {
+  extern __shared__ __align__(1024) uint8_t dsmem[];
+  AtBwdShared& sh = *reinterpret_cast<AtBwdShared*>(dsmem + AtBwdTile<D>::smem);
+  const uint32_t smem = smem_u32(dsmem);
+  at_zero_tails<D>(dsmem + AtBwdTile<D>::ring_a, kAtSlotsA + kAtSlotsB, a.tpt * a.G);
+  fence_proxy_async_shared();
+  const uint32_t tmem = at_bwd_begin(sh);
+  const bool misaligned = (smem & 1023u) != 0;
+  if (misaligned && threadIdx.x == 0) raise_status(a.status, 4 /* BI_ERR_CUDA */);
+  const int64_t nu = misaligned ? 0 : static_cast<int64_t>(a.head->nunits) * a.Hkv;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp < 8) {
+    at_dkv_probs<D>(sh, a, nu, tmem);
+  } else if (warp == 8) {
+    if (lane == 0) at_dkv_load<D>(sh, a, smem, nu, &mq, &mk, &mv, &mdo);
+    __syncwarp();
+  } else {
+    at_dkv_mma<D>(sh, a, dsmem, nu, tmem);
+  }
+  at_bwd_end(sh, tmem);
+}
+
+// ----------------------------------------------------------------------------------------------
+// dQ: query rows are the lanes, keys the columns
+// ----------------------------------------------------------------------------------------------
+// Tensor memory: S twice, dP, dQ.  dS replaces the scores and is the A operand of dQ.  S runs two
+// tiles ahead, so the exponentials of a tile never wait for its products.
+struct AtQUnit {
+  AttnSeq q;
+  int32_t h, t0;
+  int32_t n;        // key tiles that a row of the unit sees
+};
+__device__ __forceinline__ AtQUnit at_q_unit(const AttnBwdArgs& a, int64_t u) {
+  AtQUnit x;
+  const AttnUnit w = a.units[u / a.Hkv];
+  x.h = static_cast<int32_t>(u % a.Hkv);
+  x.q = a.seqs[w.seq];
+  x.t0 = w.t0;
+  const int32_t last = (w.t0 + a.tpt < x.q.lq ? w.t0 + a.tpt : x.q.lq) - 1;
+  x.n = (attn_visible(last, x.q.lq, x.q.lk, a.causal) + kAtTile - 1) / kAtTile;
+  return x;
+}
+
+template <int D>
+__device__ __forceinline__ void at_dq_load(AtBwdShared& sh, const AttnBwdArgs& a, uint32_t smem, int64_t nu,
+                                           const CUtensorMap* mq, const CUtensorMap* mk, const CUtensorMap* mv,
+                                           const CUtensorMap* mdo) {
+  using T = AtBwdTile<D>;
+  const WaitCtl wc{&sh.abort_flag, a.status, a.limit_ns};
+  tma_prefetch_desc(mq);
+  tma_prefetch_desc(mk);
+  tma_prefetch_desc(mv);
+  tma_prefetch_desc(mdo);
+  const uint32_t bytes = static_cast<uint32_t>(a.tpt * a.G) * 128u * (D / 64);
+  AtRing<kAtSlotsA> ra;
+  AtRing<kAtSlotsB> rb;
+  uint32_t hph = 0;
+  for (int64_t u = blockIdx.x; u < nu; u += gridDim.x) {
+    const AtQUnit x = at_q_unit(a, u);
+    if (x.n == 0) continue;
+    if (!mbar_wait<false>(&sh.held_empty, hph ^ 1u, wc)) return;
+    hph ^= 1u;
+    mbar_arrive_expect_tx(&sh.held_full, 2 * bytes);
+    const int32_t row = static_cast<int32_t>(x.q.q0) + x.t0;
+#pragma unroll
+    for (int b = 0; b < D / 64; ++b) {
+      tma_load_3d(smem + b * kAUnitBytes, mq, &sh.held_full, b * 64, x.h * a.G, row);
+      tma_load_3d(smem + T::tile_bytes + b * kAUnitBytes, mdo, &sh.held_full, b * 64, x.h * a.G, row);
+    }
+    auto key_tile = [&](int32_t j) {
+      if (!mbar_wait<false>(&sh.a_empty[ra.slot], ra.phase ^ 1u, wc)) return false;
+      mbar_arrive_expect_tx(&sh.a_full[ra.slot], T::tile_bytes);
+#pragma unroll
+      for (int b = 0; b < D / 64; ++b)
+        tma_load_3d(smem + T::ring_a + ra.slot * T::tile_bytes + b * kAUnitBytes, mk, &sh.a_full[ra.slot], b * 64, x.h,
+                    static_cast<int32_t>(x.q.k0) + j * kAtTile);
+      ra.next();
+      return true;
+    };
+    if (!key_tile(0)) return;
+    for (int32_t j = 0; j < x.n; ++j) {  // in the order of use: V_j behind K_j, before K_{j+1}
+      if (!mbar_wait<false>(&sh.b_empty[rb.slot], rb.phase ^ 1u, wc)) return;
+      mbar_arrive_expect_tx(&sh.b_full[rb.slot], T::tile_bytes);
+#pragma unroll
+      for (int b = 0; b < D / 64; ++b)
+        tma_load_3d(smem + T::ring_b + rb.slot * T::tile_bytes + b * kAUnitBytes, mv, &sh.b_full[rb.slot], b * 64, x.h,
+                    static_cast<int32_t>(x.q.k0) + j * kAtTile);
+      rb.next();
+      if (j + 1 < x.n && !key_tile(j + 1)) return;
+    }
+  }
+}
+
+template <int D>
+__device__ __forceinline__ void at_dq_mma(AtBwdShared& sh, const AttnBwdArgs& a, uint8_t* smem_p, int64_t nu,
+                                          uint32_t tmem) {
+  using T = AtBwdTile<D>;
+  const WaitCtl wc{&sh.abort_flag, a.status, a.limit_ns};
+  const uint32_t smem = smem_u32(smem_p);
+  const int lane = threadIdx.x & 31;
+  constexpr uint32_t ts = T::tile_bytes >> 4;
+  const uint64_t dq = sdesc_k_sw128(smem), ddo = sdesc_k_sw128(smem + T::tile_bytes);
+  const uint64_t dk_k = sdesc_k_sw128(smem + T::ring_a), dk_mn = sdesc_mn_sw128(smem + T::ring_a, kAUnitBytes);
+  const uint64_t dv_k = sdesc_k_sw128(smem + T::ring_b);
+  const uint32_t t_dp = tmem + 256, t_dq = tmem + 384;
+  AtRing<kAtSlotsA> ra, ra2;
+  AtRing<kAtSlotsB> rb;
+  AtRing<2> sb;                // score buffer of the next S
+  uint32_t hph = 0, ph = 0, cur = 0;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    const bool ok = __all_sync(0xffffffffu, mbar_wait<false>(bar, parity, wc));
+    tc_fence_after();
+    return ok;
+  };
+  for (int64_t u = blockIdx.x; u < nu; u += gridDim.x) {
+    const AtQUnit x = at_q_unit(a, u);
+    if (x.n == 0) continue;
+    auto scores = [&](int32_t j) {
+      if (!wait(&sh.a_full[ra.slot], ra.phase)) return false;
+      const int32_t rows = x.q.lk - j * kAtTile;
+      if (rows < kAtTile) at_zero_rows<D>(smem_p + T::ring_a + ra.slot * T::tile_bytes, rows);
+      if (lane == 0) {
+        at_mma_ss<D>(tmem + sb.slot * 128, dq, dk_k + ra.slot * ts);
+        umma_commit(&sh.s_full[sb.slot]);
+      }
+      ra.next();
+      sb.next();
+      return true;
+    };
+    auto dprobs = [&](int32_t j) {
+      if (!wait(&sh.b_full[rb.slot], rb.phase)) return false;
+      if (lane == 0) {
+        at_mma_ss<D>(t_dp, ddo, dv_k + rb.slot * ts);
+        umma_commit(&sh.dp_full);
+        umma_commit(&sh.b_empty[rb.slot]);
+      }
+      rb.next();
+      return true;
+    };
+    if (!wait(&sh.held_full, hph)) break;
+    hph ^= 1u;
+    if (!scores(0) || !dprobs(0)) break;
+    if (x.n > 1 && !scores(1)) break;
+    if (x.n == 1 && lane == 0) umma_commit(&sh.held_empty);
+    bool ok = true;
+    for (int32_t j = 0; j < x.n && ok; ++j) {
+      // One barrier for the whole tile: dP_{j+1} lets the next dS come, so nothing of this one may
+      // still be waited for behind it.
+      if (!wait(&sh.ds_full[0], ph)) { ok = false; break; }
+      if (j + 1 < x.n) {
+        if (!dprobs(j + 1)) { ok = false; break; }
+        if (j + 2 == x.n && lane == 0) umma_commit(&sh.held_empty);
+      }
+      if (lane == 0) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+          at_mma_ts<D>(t_dq, tmem + cur * 128, dk_mn + ra2.slot * ts, half, j == 0);
+        umma_commit(&sh.a_empty[ra2.slot]);
+        if (j + 1 == x.n) umma_commit(&sh.acc_full);
+      }
+      ra2.next();
+      cur ^= 1u;
+      ph ^= 1u;
+      if (j + 2 < x.n && !scores(j + 2)) ok = false;
+    }
+    if (!ok) break;
+  }
+  __syncwarp();
+  if (lane == 0) umma_commit(&sh.done);
+  mbar_wait<false>(&sh.done, 0u, wc);
+}
+
+template <int D>
+__device__ __forceinline__ void at_dq_probs(AtBwdShared& sh, const AttnBwdArgs& a, int64_t nu, uint32_t tmem) {
+  const WaitCtl wc{&sh.abort_flag, a.status, a.limit_ns};
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int X = warp >> 2, row = (warp & 3) * 32 + lane;
+  const int tok_in = row / a.G, g = row - tok_in * a.G;
+  const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+  const uint32_t t_s = tmem + lanes + X * 32, t_dp = t_s + 256;
+  uint32_t ph = 0, aph = 0;
+  AtRing<2> sb;
+  const float2 cc = make_float2(a.c, a.c);
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    const bool ok = __all_sync(0xffffffffu, mbar_wait<false>(bar, parity, wc));
+    tc_fence_after();
+    return ok;
+  };
+  for (int64_t u = blockIdx.x; u < nu; u += gridDim.x) {
+    const AtQUnit x = at_q_unit(a, u);
+    const int32_t tok = x.t0 + tok_in;
+    const bool valid = tok_in < a.tpt && tok < x.q.lq;
+    const int32_t vis = valid ? attn_visible(tok, x.q.lq, x.q.lk, a.causal) : 0;
+    uint16_t* o = a.o0 + (x.q.q0 + tok) * a.ld0 + static_cast<int64_t>(x.h * a.G + g) * D + X * (D / 2);
+    if (x.n == 0) {  // no key to see
+      if (valid)
+#pragma unroll
+        for (int b = 0; b < D / 64; ++b) at_zero32(o + b * 32);
+      continue;
+    }
+    const float* st = a.st + (x.h * a.tiles + x.q.unit0 + x.t0 / a.tpt) * (2 * kAtTile) + row;
+    const float2 nl = make_float2(st[0], st[0]), nd = make_float2(st[kAtTile], st[kAtTile]);
+    for (int32_t j = 0; j < x.n; ++j) {
+      const int32_t lim = vis - j * kAtTile;  // columns from here on are not seen
+      const bool masked = __any_sync(0xffffffffu, lim < kAtTile);
+      if (!wait(&sh.s_full[sb.slot], sb.phase)) return;
+      uint32_t s[2][32];
+      float2 p[2][16];
+      at_get(t_s + sb.slot * 128, s);
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        if (masked)
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (half * 64 + X * 32 + e >= lim) s[half][e] = 0xff800000u;  // -inf
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const float2 y = fma2(at_pair(s[half], e), cc, nl);
+          p[half][e] = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+        }
+      }
+      if (!wait(&sh.dp_full, ph)) return;
+      at_get(t_dp, s);
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        if (masked)
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (half * 64 + X * 32 + e >= lim) s[half][e] = 0u;  // what v holds there does not matter
+#pragma unroll
+        for (int e = 0; e < 16; ++e) p[half][e] = mul2(p[half][e], add2(at_pair(s[half], e), nd));
+        at_put(t_s + sb.slot * 128 + half * 64, p[half]);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(&sh.ds_full[0]);
+      sb.next();
+      ph ^= 1u;
+    }
+    if (!wait(&sh.acc_full, aph)) return;
+    aph ^= 1u;
+#pragma unroll 1
+    for (int b = 0; b < D / 64; ++b)
+      at_store32(tmem + lanes + 384 + X * (D / 2) + b * 32, a.scale, o + b * 32, valid);
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kAtBwdThreads, 1)
+    k_attn_dq(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+              const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mdo, const AttnBwdArgs a) {
+  extern __shared__ __align__(1024) uint8_t dsmem[];
+  AtBwdShared& sh = *reinterpret_cast<AtBwdShared*>(dsmem + AtBwdTile<D>::smem);
+  const uint32_t smem = smem_u32(dsmem);
+  const uint32_t tmem = at_bwd_begin(sh);
+  const bool misaligned = (smem & 1023u) != 0;
+  if (misaligned && threadIdx.x == 0) raise_status(a.status, 4 /* BI_ERR_CUDA */);
+  const int64_t nu = misaligned ? 0 : static_cast<int64_t>(a.head->nunits) * a.Hkv;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp < 8) {
+    at_dq_probs<D>(sh, a, nu, tmem);
+  } else if (warp == 8) {
+    if (lane == 0) at_dq_load<D>(sh, a, smem, nu, &mq, &mk, &mv, &mdo);
+    __syncwarp();
+  } else {
+    at_dq_mma<D>(sh, a, dsmem, nu, tmem);
+  }
+  at_bwd_end(sh, tmem);
+}
+
+}  // namespace bi

@@ -132,6 +132,29 @@ BI_API bi_status bi_attn_fwd(const uint16_t* q, const uint16_t* k, const uint16_
                              float scale, uint16_t* out, float* lse, int32_t* dev_status, void* ws, size_t ws_bytes,
                              void* stream);
 
+/*
+ * Its gradient: dq [Tq][Hq][D], dk, dv [Tk][Hkv][D] bf16 (tokens dq_ld, dk_ld, dv_ld elements apart, so they
+ * may be slices of one buffer) of sum(out * dout), overwritten.  q, k, v, the offsets, causal and scale as in
+ * the forward, out and lse its results; dout [Tq][Hq][D] bf16 with dout_ld elements between tokens.  The
+ * probabilities are recomputed: p_ij = exp(scale q_i . k_j - lse_i); with delta_i = dout_i . out_i and
+ * ds_ij = p_ij (dout_i . v_j - delta_i),
+ *   dv_j = sum_i p_ij dout_i,   dk_j = scale sum_i ds_ij q_i,   dq_i = scale sum_j ds_ij k_j,
+ * the sums over i running over all query heads of the key/value head.  p and ds are rounded to bf16 for
+ * their products, sums are fp32 in an order that depends on the places in the sequence only: no atomics, and
+ * a sequence's gradients have the same bits in any batch.  A query that sees no key, and a key that no query
+ * sees, get zeros; rows in no sequence (and cache rows behind k_lens) are left as they were.
+ * dq, dk and dv may overlap neither each other nor an input.  A NaN or infinity in a row of a sequence
+ * stays in that sequence.  Errors as in the forward, for a ws of bi_attn_bwd_workspace_bytes(...).
+ */
+BI_API size_t bi_attn_bwd_workspace_bytes(int64_t Tq, int64_t Tk, int32_t S, int32_t Hq, int32_t Hkv, int32_t D);
+BI_API bi_status bi_attn_bwd(const uint16_t* dout, int64_t dout_ld, const uint16_t* q, const uint16_t* k,
+                             const uint16_t* v, int64_t q_ld, int64_t k_ld, int64_t v_ld, const uint16_t* out,
+                             const float* lse, const int64_t* q_offsets, const int64_t* k_offsets,
+                             const int32_t* k_lens, int32_t S, int64_t Tq, int64_t Tk, int32_t Hq, int32_t Hkv,
+                             int32_t D, int32_t causal, float scale, uint16_t* dq, uint16_t* dk, uint16_t* dv,
+                             int64_t dq_ld, int64_t dk_ld, int64_t dv_ld, int32_t* dev_status, void* ws,
+                             size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
