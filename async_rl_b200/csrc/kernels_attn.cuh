@@ -265,6 +265,14 @@ __device__ __forceinline__ float attn_join_scale(float from, float to) {
   return to == -INFINITY ? 0.f : ex2_approx(from - to);
 }
 
+// A CTA's r-th unit.  Units are listed dearest first; every other round runs backwards, so that a CTA
+// that began with a dear one ends with a cheap one.
+__device__ __forceinline__ int64_t at_turn(int64_t r) {
+  return r * gridDim.x + ((r & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+}
+// Keeps a rarely taken branch a branch: its selects are not to be executed everywhere.
+__device__ __forceinline__ void at_rare() { asm volatile("" ::: "memory"); }
+
 // What every role derives from a unit.
 struct AtUnit {
   AttnSeq q;
@@ -304,7 +312,7 @@ __device__ __forceinline__ void at_fwd_load(AtFwdShared& sh, const AttnFwdArgs& 
   const uint32_t ring = smem + 2 * T::tile_bytes;
   const uint32_t qbytes = static_cast<uint32_t>(a.tpt * a.G) * 128u * (D / 64);
   uint32_t slot = 0, phase = 0, qph = 0;
-  for (int64_t u = blockIdx.x; u < nu; u += gridDim.x) {
+  for (int64_t r = 0, u; (u = at_turn(r)) < nu; ++r) {
     const AtUnit x = at_unit(a, u);
     if (x.n <= x.jb) continue;
     if (!mbar_wait<false>(&sh.q_empty, qph ^ 1u, wc)) return;
@@ -350,7 +358,6 @@ __device__ __forceinline__ void at_fwd_mma(AtFwdShared& sh, const AttnFwdArgs& a
   using T = AtFwdTile<D>;
   const WaitCtl wc{&sh.abort_flag, a.status, a.limit_ns};
   const uint32_t smem = smem_u32(smem_p);
-  const int lane = threadIdx.x & 31;
   constexpr uint32_t idesc_s = idesc_bf16(128, 128, false, false);
   constexpr uint32_t idesc_o = idesc_bf16(128, D, false, true);
   constexpr uint64_t blk = kAUnitBytes >> 4;
@@ -359,7 +366,7 @@ __device__ __forceinline__ void at_fwd_mma(AtFwdShared& sh, const AttnFwdArgs& a
   const uint64_t dv0 = sdesc_mn_sw128(smem + 2 * T::tile_bytes, kAUnitBytes);
   uint32_t slot = 0, phase = 0, qph = 0, pph[2] = {0, 0};
   auto scores = [&](int X, uint32_t ks) {  // S_X = Q_X K^T
-    if (lane == 0) {
+    if (elect_one()) {
       const uint64_t da = dq0 + X * (T::tile_bytes >> 4), db = dk0 + ks * (T::tile_bytes >> 4);
 #pragma unroll
       for (int b = 0; b < D / 64; ++b)
@@ -370,7 +377,7 @@ __device__ __forceinline__ void at_fwd_mma(AtFwdShared& sh, const AttnFwdArgs& a
     }
   };
   auto values = [&](int X, uint32_t vs, bool first) {  // O_X += P_X V
-    if (lane == 0) {
+    if (elect_one()) {
       const uint64_t db = dv0 + vs * (T::tile_bytes >> 4);
 #pragma unroll
       for (int k = 0; k < 8; ++k)
@@ -378,7 +385,7 @@ __device__ __forceinline__ void at_fwd_mma(AtFwdShared& sh, const AttnFwdArgs& a
                      (k > 0 || !first) ? 1u : 0u);
     }
   };
-  for (int64_t u = blockIdx.x; u < nu; u += gridDim.x) {
+  for (int64_t r = 0, u; (u = at_turn(r)) < nu; ++r) {
     const AtUnit x = at_unit(a, u);
     if (x.n <= x.jb) continue;
     if (!__all_sync(0xffffffffu, mbar_wait<false>(&sh.q_full, qph, wc))) break;
@@ -387,7 +394,7 @@ __device__ __forceinline__ void at_fwd_mma(AtFwdShared& sh, const AttnFwdArgs& a
     tc_fence_after();
     for (int X = 0; X < 2; ++X)
       if (x.jb < x.je[X]) scores(X, slot);
-    if (lane == 0) {
+    if (elect_one()) {
       umma_commit(&sh.empty[slot]);
       if (x.jb + 1 == x.n) umma_commit(&sh.q_empty);
     }
@@ -410,7 +417,7 @@ __device__ __forceinline__ void at_fwd_mma(AtFwdShared& sh, const AttnFwdArgs& a
           pph[X] ^= 1u;
           tc_fence_after();
           values(X, vs, first);
-          if (lane == 0 && (last || j + 1 == x.je[X])) umma_commit(&sh.o_full[X]);
+          if (elect_one() && (last || j + 1 == x.je[X])) umma_commit(&sh.o_full[X]);
         }
         if (next && !have_k) {
           if (!__all_sync(0xffffffffu, mbar_wait<false>(&sh.full[slot], phase, wc))) { ok = false; break; }
@@ -420,7 +427,7 @@ __device__ __forceinline__ void at_fwd_mma(AtFwdShared& sh, const AttnFwdArgs& a
         if (j + 1 < x.je[X]) scores(X, slot);
       }
       if (!ok) break;
-      if (lane == 0) {
+      if (elect_one()) {
         umma_commit(&sh.empty[vs]);
         if (next) umma_commit(&sh.empty[slot]);
         if (j + 2 == x.n) umma_commit(&sh.q_empty);
@@ -430,7 +437,7 @@ __device__ __forceinline__ void at_fwd_mma(AtFwdShared& sh, const AttnFwdArgs& a
     if (!ok) break;
   }
   __syncwarp();
-  if (lane == 0) umma_commit(&sh.done);
+  if (elect_one()) umma_commit(&sh.done);
   mbar_wait<false>(&sh.done, 0u, wc);
 }
 
@@ -446,7 +453,7 @@ __device__ __forceinline__ void at_fwd_softmax(AtFwdShared& sh, const AttnFwdArg
   const int tok_in = row / a.G, g = row - tok_in * a.G;
   float4* scr = reinterpret_cast<float4*>(a.scratch) + ((static_cast<int64_t>(blockIdx.x) * 2 + X) * (D / 4)) * 128 + row;
   uint32_t sph = 0, oph = 0;
-  for (int64_t u = blockIdx.x; u < nu; u += gridDim.x) {
+  for (int64_t r = 0, u; (u = at_turn(r)) < nu; ++r) {
     const AtUnit x = at_unit(a, u);
     const int32_t tok = x.t0 + X * a.tpt + tok_in;
     const bool valid = tok_in < a.tpt && tok < x.q.lq;
@@ -481,6 +488,7 @@ __device__ __forceinline__ void at_fwd_softmax(AtFwdShared& sh, const AttnFwdArg
         for (int b = 0; b < 4; ++b) tmem_ld_pin(s[b]);
         const int32_t lim = vis - j * kAtTile;
         if (__any_sync(0xffffffffu, lim < kAtTile)) {
+          at_rare();
 #pragma unroll
           for (int b = 0; b < 4; ++b)
 #pragma unroll

@@ -271,7 +271,7 @@ __device__ __forceinline__ void at_dkv_load(AtBwdShared& sh, const AttnBwdArgs& 
   AtRing<kAtSlotsB> rb;
   AtRing<2> rs;
   uint32_t hph = 0;
-  for (int64_t u = blockIdx.x; u < nu; u += gridDim.x) {
+  for (int64_t r = 0, u; (u = at_turn(r)) < nu; ++r) {
     const AtKvUnit x = at_kv_unit(a, u);
     if (x.i0 >= x.i1) continue;
     if (!mbar_wait<false>(&sh.held_empty, hph ^ 1u, wc)) return;
@@ -315,7 +315,6 @@ __device__ __forceinline__ void at_dkv_mma(AtBwdShared& sh, const AttnBwdArgs& a
   using T = AtBwdTile<D>;
   const WaitCtl wc{&sh.abort_flag, a.status, a.limit_ns};
   const uint32_t smem = smem_u32(smem_p);
-  const int lane = threadIdx.x & 31;
   constexpr uint32_t ts = T::tile_bytes >> 4;
   const uint64_t dk = sdesc_k_sw128(smem), dv = sdesc_k_sw128(smem + T::tile_bytes);
   const uint64_t dq_k = sdesc_k_sw128(smem + T::ring_a), dq_mn = sdesc_mn_sw128(smem + T::ring_a, kAUnitBytes);
@@ -330,7 +329,7 @@ __device__ __forceinline__ void at_dkv_mma(AtBwdShared& sh, const AttnBwdArgs& a
     tc_fence_after();
     return ok;
   };
-  for (int64_t u = blockIdx.x; u < nu; u += gridDim.x) {
+  for (int64_t r = 0, u; (u = at_turn(r)) < nu; ++r) {
     const AtKvUnit x = at_kv_unit(a, u);
     if (x.i0 >= x.i1) continue;
     // rows behind the sequence's last query may be another sequence's, or hold anything: zeros
@@ -338,7 +337,7 @@ __device__ __forceinline__ void at_dkv_mma(AtBwdShared& sh, const AttnBwdArgs& a
     auto scores = [&](int32_t i) {
       if (!wait(&sh.a_full[ra.slot], ra.phase)) return false;
       if (i + 1 == x.i1) at_zero_rows<D>(smem_p + T::ring_a + ra.slot * T::tile_bytes, last_rows);
-      if (lane == 0) {
+      if (elect_one()) {
         at_mma_ss<D>(t_s, dk, dq_k + ra.slot * ts);
         umma_commit(&sh.s_full[0]);
       }
@@ -348,7 +347,7 @@ __device__ __forceinline__ void at_dkv_mma(AtBwdShared& sh, const AttnBwdArgs& a
     auto dprobs = [&](int32_t i) {
       if (!wait(&sh.b_full[rb.slot], rb.phase)) return false;
       if (i + 1 == x.i1) at_zero_rows<D>(smem_p + T::ring_b + rb.slot * T::tile_bytes, last_rows);
-      if (lane == 0) {
+      if (elect_one()) {
         at_mma_ss<D>(t_dp, dv, do_k + rb.slot * ts);
         umma_commit(&sh.dp_full);
         if (i + 1 == x.i1) umma_commit(&sh.held_empty);
@@ -365,19 +364,19 @@ __device__ __forceinline__ void at_dkv_mma(AtBwdShared& sh, const AttnBwdArgs& a
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         ok = ok && wait(&sh.p_full[half], ph);
-        if (ok && lane == 0) at_mma_ts<D>(t_dv, t_s, do_mn + rb2.slot * ts, half, first);
+        if (ok && elect_one()) at_mma_ts<D>(t_dv, t_s, do_mn + rb2.slot * ts, half, first);
       }
       if (!ok) break;
-      if (lane == 0) umma_commit(&sh.b_empty[rb2.slot]);
+      if (elect_one()) umma_commit(&sh.b_empty[rb2.slot]);
       rb2.next();
       if (next && !scores(i + 1)) ok = false;
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         ok = ok && wait(&sh.ds_full[half], ph);
-        if (ok && lane == 0) at_mma_ts<D>(t_dk, t_dp, dq_mn + ra2.slot * ts, half, first);
+        if (ok && elect_one()) at_mma_ts<D>(t_dk, t_dp, dq_mn + ra2.slot * ts, half, first);
       }
       if (!ok) break;
-      if (lane == 0) {
+      if (elect_one()) {
         umma_commit(&sh.a_empty[ra2.slot]);
         umma_commit(&sh.st_empty[rs.slot]);
         if (!next) umma_commit(&sh.acc_full);
@@ -390,7 +389,7 @@ __device__ __forceinline__ void at_dkv_mma(AtBwdShared& sh, const AttnBwdArgs& a
     if (!ok) break;
   }
   __syncwarp();
-  if (lane == 0) umma_commit(&sh.done);
+  if (elect_one()) umma_commit(&sh.done);
   mbar_wait<false>(&sh.done, 0u, wc);
 }
 
@@ -410,7 +409,7 @@ __device__ __forceinline__ void at_dkv_probs(AtBwdShared& sh, const AttnBwdArgs&
     tc_fence_after();
     return ok;
   };
-  for (int64_t u = blockIdx.x; u < nu; u += gridDim.x) {
+  for (int64_t r = 0, u; (u = at_turn(r)) < nu; ++r) {
     const AtKvUnit x = at_kv_unit(a, u);
     const int32_t key = x.t0 + key_in;
     const bool valid = key < x.q.lk;
@@ -437,10 +436,12 @@ __device__ __forceinline__ void at_dkv_probs(AtBwdShared& sh, const AttnBwdArgs&
       at_get(t_s, s);
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        if (masked)
+        if (masked) {
+          at_rare();
 #pragma unroll
           for (int e = 0; e < 32; ++e)
             if (half * 64 + X * 32 + e < low) s[half][e] = 0xff800000u;  // -inf
+        }
 #pragma unroll
         for (int e = 0; e < 16; e += 2) {
           const float4 l = nl[half * 16 + e / 2];
@@ -458,10 +459,12 @@ __device__ __forceinline__ void at_dkv_probs(AtBwdShared& sh, const AttnBwdArgs&
       at_get(t_dp, s);
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        if (masked)
+        if (masked) {
+          at_rare();
 #pragma unroll
           for (int e = 0; e < 32; ++e)
             if (half * 64 + X * 32 + e < low) s[half][e] = 0u;  // p is 0 there; what v holds does not matter
+        }
 #pragma unroll
         for (int e = 0; e < 16; e += 2) {
           const float4 d = nd[half * 16 + e / 2];
@@ -553,7 +556,7 @@ __device__ __forceinline__ void at_dq_load(AtBwdShared& sh, const AttnBwdArgs& a
   AtRing<kAtSlotsA> ra;
   AtRing<kAtSlotsB> rb;
   uint32_t hph = 0;
-  for (int64_t u = blockIdx.x; u < nu; u += gridDim.x) {
+  for (int64_t r = 0, u; (u = at_turn(r)) < nu; ++r) {
     const AtQUnit x = at_q_unit(a, u);
     if (x.n == 0) continue;
     if (!mbar_wait<false>(&sh.held_empty, hph ^ 1u, wc)) return;
@@ -595,7 +598,6 @@ __device__ __forceinline__ void at_dq_mma(AtBwdShared& sh, const AttnBwdArgs& a,
   using T = AtBwdTile<D>;
   const WaitCtl wc{&sh.abort_flag, a.status, a.limit_ns};
   const uint32_t smem = smem_u32(smem_p);
-  const int lane = threadIdx.x & 31;
   constexpr uint32_t ts = T::tile_bytes >> 4;
   const uint64_t dq = sdesc_k_sw128(smem), ddo = sdesc_k_sw128(smem + T::tile_bytes);
   const uint64_t dk_k = sdesc_k_sw128(smem + T::ring_a), dk_mn = sdesc_mn_sw128(smem + T::ring_a, kAUnitBytes);
@@ -610,14 +612,14 @@ __device__ __forceinline__ void at_dq_mma(AtBwdShared& sh, const AttnBwdArgs& a,
     tc_fence_after();
     return ok;
   };
-  for (int64_t u = blockIdx.x; u < nu; u += gridDim.x) {
+  for (int64_t r = 0, u; (u = at_turn(r)) < nu; ++r) {
     const AtQUnit x = at_q_unit(a, u);
     if (x.n == 0) continue;
     auto scores = [&](int32_t j) {
       if (!wait(&sh.a_full[ra.slot], ra.phase)) return false;
       const int32_t rows = x.q.lk - j * kAtTile;
       if (rows < kAtTile) at_zero_rows<D>(smem_p + T::ring_a + ra.slot * T::tile_bytes, rows);
-      if (lane == 0) {
+      if (elect_one()) {
         at_mma_ss<D>(tmem + sb.slot * 128, dq, dk_k + ra.slot * ts);
         umma_commit(&sh.s_full[sb.slot]);
       }
@@ -627,7 +629,7 @@ __device__ __forceinline__ void at_dq_mma(AtBwdShared& sh, const AttnBwdArgs& a,
     };
     auto dprobs = [&](int32_t j) {
       if (!wait(&sh.b_full[rb.slot], rb.phase)) return false;
-      if (lane == 0) {
+      if (elect_one()) {
         at_mma_ss<D>(t_dp, ddo, dv_k + rb.slot * ts);
         umma_commit(&sh.dp_full);
         umma_commit(&sh.b_empty[rb.slot]);
@@ -639,7 +641,7 @@ __device__ __forceinline__ void at_dq_mma(AtBwdShared& sh, const AttnBwdArgs& a,
     hph ^= 1u;
     if (!scores(0) || !dprobs(0)) break;
     if (x.n > 1 && !scores(1)) break;
-    if (x.n == 1 && lane == 0) umma_commit(&sh.held_empty);
+    if (x.n == 1 && elect_one()) umma_commit(&sh.held_empty);
     bool ok = true;
     for (int32_t j = 0; j < x.n && ok; ++j) {
       // One barrier for the whole tile: dP_{j+1} lets the next dS come, so nothing of this one may
@@ -647,9 +649,9 @@ __device__ __forceinline__ void at_dq_mma(AtBwdShared& sh, const AttnBwdArgs& a,
       if (!wait(&sh.ds_full[0], ph)) { ok = false; break; }
       if (j + 1 < x.n) {
         if (!dprobs(j + 1)) { ok = false; break; }
-        if (j + 2 == x.n && lane == 0) umma_commit(&sh.held_empty);
+        if (j + 2 == x.n && elect_one()) umma_commit(&sh.held_empty);
       }
-      if (lane == 0) {
+      if (elect_one()) {
 #pragma unroll
         for (int half = 0; half < 2; ++half)
           at_mma_ts<D>(t_dq, tmem + cur * 128, dk_mn + ra2.slot * ts, half, j == 0);
@@ -664,7 +666,7 @@ __device__ __forceinline__ void at_dq_mma(AtBwdShared& sh, const AttnBwdArgs& a,
     if (!ok) break;
   }
   __syncwarp();
-  if (lane == 0) umma_commit(&sh.done);
+  if (elect_one()) umma_commit(&sh.done);
   mbar_wait<false>(&sh.done, 0u, wc);
 }
 
@@ -684,7 +686,7 @@ __device__ __forceinline__ void at_dq_probs(AtBwdShared& sh, const AttnBwdArgs& 
     tc_fence_after();
     return ok;
   };
-  for (int64_t u = blockIdx.x; u < nu; u += gridDim.x) {
+  for (int64_t r = 0, u; (u = at_turn(r)) < nu; ++r) {
     const AtQUnit x = at_q_unit(a, u);
     const int32_t tok = x.t0 + tok_in;
     const bool valid = tok_in < a.tpt && tok < x.q.lq;
@@ -707,10 +709,12 @@ __device__ __forceinline__ void at_dq_probs(AtBwdShared& sh, const AttnBwdArgs& 
       at_get(t_s + sb.slot * 128, s);
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        if (masked)
+        if (masked) {
+          at_rare();
 #pragma unroll
           for (int e = 0; e < 32; ++e)
             if (half * 64 + X * 32 + e >= lim) s[half][e] = 0xff800000u;  // -inf
+        }
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           const float2 y = fma2(at_pair(s[half], e), cc, nl);
@@ -721,10 +725,12 @@ __device__ __forceinline__ void at_dq_probs(AtBwdShared& sh, const AttnBwdArgs& 
       at_get(t_dp, s);
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        if (masked)
+        if (masked) {
+          at_rare();
 #pragma unroll
           for (int e = 0; e < 32; ++e)
             if (half * 64 + X * 32 + e >= lim) s[half][e] = 0u;  // what v holds there does not matter
+        }
 #pragma unroll
         for (int e = 0; e < 16; ++e) p[half][e] = mul2(p[half][e], add2(at_pair(s[half], e), nd));
         at_put(t_s + sb.slot * 128 + half * 64, p[half]);
