@@ -273,6 +273,13 @@ __device__ __forceinline__ int64_t at_turn(int64_t r) {
 // Keeps a rarely taken branch a branch: its selects are not to be executed everywhere.
 __device__ __forceinline__ void at_rare() { asm volatile("" ::: "memory"); }
 
+// A warp's wait for what MMAs left in tensor memory or what another role wrote.
+__device__ __forceinline__ bool at_wait(uint64_t* bar, uint32_t parity, const WaitCtl& wc) {
+  const bool ok = __all_sync(0xffffffffu, mbar_wait<false>(bar, parity, wc));
+  tc_fence_after();
+  return ok;
+}
+
 // What every role derives from a unit.
 struct AtUnit {
   AttnSeq q;

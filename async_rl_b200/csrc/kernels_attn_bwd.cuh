@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(kAtPreThreads) k_attn_pre(const AttnBwdArgs a)
 // ----------------------------------------------------------------------------------------------
 // shared by both kernels
 // ----------------------------------------------------------------------------------------------
-constexpr int kAtBwdThreads = 320;  // warps 0-7: p and ds; 8: TMA; 9: MMA
+constexpr int kAtBwdThreads = 352;  // warps 0-7: p and ds; 8: TMA; 9: MMA; 10: ragged tiles
 constexpr int kAtSlotsA = 3, kAtSlotsB = 2;
 
 template <int D>
@@ -112,6 +112,7 @@ struct AtBwdShared {
   uint64_t s_full[2], dp_full;
   uint64_t p_full[2], ds_full[2];  // halves of the columns (dQ: ds_full[0] for both)
   uint64_t acc_full, done;
+  uint64_t z_ask[2], z_full[2];    // a unit's ragged last tile (A and B ring): loading; has its zeros
   uint32_t tmem_base;
   volatile uint32_t abort_flag;
 };
@@ -122,6 +123,10 @@ template <int N>
 struct AtRing {
   uint32_t slot = 0, phase = 0;
   __device__ __forceinline__ void next() { ring_advance(slot, phase, N); }
+  __device__ __forceinline__ void skip(uint32_t n) {
+    phase ^= ((slot + n) / N) & 1u;
+    slot = (slot + n) % N;
+  }
 };
 
 // Warp roles' common start and end; returns the base of tensor memory.
@@ -139,6 +144,8 @@ __device__ __forceinline__ uint32_t at_bwd_begin(AtBwdShared& sh) {
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.st_full[i], 1);
+      mbar_init(&sh.z_ask[i], 1);
+      mbar_init(&sh.z_full[i], 1);
       mbar_init(&sh.st_empty[i], 1);
       mbar_init(&sh.s_full[i], 1);
       mbar_init(&sh.p_full[i], 256);
@@ -242,6 +249,8 @@ struct AtKvUnit {
   int32_t h, t0;
   int32_t i0, i1;   // query tiles that see a key of the unit
   int64_t tile0;    // of the sequence's first query tile
+  int32_t rows;     // of the last query tile
+  bool ragged;
 };
 __device__ __forceinline__ AtKvUnit at_kv_unit(const AttnBwdArgs& a, int64_t u) {
   AtKvUnit x;
@@ -253,6 +262,8 @@ __device__ __forceinline__ AtKvUnit at_kv_unit(const AttnBwdArgs& a, int64_t u) 
   x.i1 = (x.q.lq + a.tpt - 1) / a.tpt;
   x.i0 = first >= x.q.lq ? x.i1 : first / a.tpt;
   x.tile0 = a.rows[w.seq].unit0;
+  x.rows = (x.q.lq - (x.i1 - 1) * a.tpt) * a.G;
+  x.ragged = x.rows < a.tpt * a.G;
   return x;
 }
 
@@ -293,6 +304,7 @@ __device__ __forceinline__ void at_dkv_load(AtBwdShared& sh, const AttnBwdArgs& 
         tma_load_3d(smem + T::ring_a + ra.slot * T::tile_bytes + b * kAUnitBytes, mq, &sh.a_full[ra.slot], b * 64,
                     x.h * a.G, row);
       ra.next();
+      if (i + 1 == x.i1 && x.ragged) mbar_arrive(&sh.z_ask[0]);
       if (!mbar_wait<false>(&sh.st_empty[rs.slot], rs.phase ^ 1u, wc)) return;
       mbar_arrive_expect_tx(&sh.st_full[rs.slot], 2 * kAtTile * 4);
       bulk_load(smem_u32(&sh.st[rs.slot][0][0]), st + static_cast<int64_t>(i) * (2 * kAtTile), 2 * kAtTile * 4,
@@ -305,16 +317,16 @@ __device__ __forceinline__ void at_dkv_load(AtBwdShared& sh, const AttnBwdArgs& 
         tma_load_3d(smem + T::ring_b + rb.slot * T::tile_bytes + b * kAUnitBytes, mdo, &sh.b_full[rb.slot], b * 64,
                     x.h * a.G, row);
       rb.next();
+      if (i + 1 == x.i1 && x.ragged) mbar_arrive(&sh.z_ask[1]);
     }
   }
 }
 
 template <int D>
-__device__ __forceinline__ void at_dkv_mma(AtBwdShared& sh, const AttnBwdArgs& a, uint8_t* smem_p, int64_t nu,
+__device__ __forceinline__ void at_dkv_mma(AtBwdShared& sh, const AttnBwdArgs& a, uint32_t smem, int64_t nu,
                                            uint32_t tmem) {
   using T = AtBwdTile<D>;
   const WaitCtl wc{&sh.abort_flag, a.status, a.limit_ns};
-  const uint32_t smem = smem_u32(smem_p);
   constexpr uint32_t ts = T::tile_bytes >> 4;
   const uint64_t dk = sdesc_k_sw128(smem), dv = sdesc_k_sw128(smem + T::tile_bytes);
   const uint64_t dq_k = sdesc_k_sw128(smem + T::ring_a), dq_mn = sdesc_mn_sw128(smem + T::ring_a, kAUnitBytes);
@@ -323,35 +335,29 @@ __device__ __forceinline__ void at_dkv_mma(AtBwdShared& sh, const AttnBwdArgs& a
   AtRing<kAtSlotsA> ra, ra2;  // next tile to arrive, tile whose dK is next
   AtRing<kAtSlotsB> rb, rb2;
   AtRing<2> rs;
-  uint32_t hph = 0, ph = 0;
+  uint32_t hph = 0, ph = 0, zph = 0;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    const bool ok = __all_sync(0xffffffffu, mbar_wait<false>(bar, parity, wc));
+    const bool ok = mbar_wait<false>(bar, parity, wc);
     tc_fence_after();
     return ok;
   };
   for (int64_t r = 0, u; (u = at_turn(r)) < nu; ++r) {
     const AtKvUnit x = at_kv_unit(a, u);
     if (x.i0 >= x.i1) continue;
-    // rows behind the sequence's last query may be another sequence's, or hold anything: zeros
-    const int last_rows = (x.q.lq - (x.i1 - 1) * a.tpt) * a.G;
     auto scores = [&](int32_t i) {
       if (!wait(&sh.a_full[ra.slot], ra.phase)) return false;
-      if (i + 1 == x.i1) at_zero_rows<D>(smem_p + T::ring_a + ra.slot * T::tile_bytes, last_rows);
-      if (elect_one()) {
-        at_mma_ss<D>(t_s, dk, dq_k + ra.slot * ts);
-        umma_commit(&sh.s_full[0]);
-      }
+      if (i + 1 == x.i1 && x.ragged && !wait(&sh.z_full[0], zph)) return false;
+      at_mma_ss<D>(t_s, dk, dq_k + ra.slot * ts);
+      umma_commit(&sh.s_full[0]);
       ra.next();
       return true;
     };
     auto dprobs = [&](int32_t i) {
       if (!wait(&sh.b_full[rb.slot], rb.phase)) return false;
-      if (i + 1 == x.i1) at_zero_rows<D>(smem_p + T::ring_b + rb.slot * T::tile_bytes, last_rows);
-      if (elect_one()) {
-        at_mma_ss<D>(t_dp, dv, do_k + rb.slot * ts);
-        umma_commit(&sh.dp_full);
-        if (i + 1 == x.i1) umma_commit(&sh.held_empty);
-      }
+      if (i + 1 == x.i1 && x.ragged && !wait(&sh.z_full[1], zph)) return false;
+      at_mma_ss<D>(t_dp, dv, do_k + rb.slot * ts);
+      umma_commit(&sh.dp_full);
+      if (i + 1 == x.i1) umma_commit(&sh.held_empty);
       rb.next();
       return true;
     };
@@ -364,33 +370,60 @@ __device__ __forceinline__ void at_dkv_mma(AtBwdShared& sh, const AttnBwdArgs& a
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         ok = ok && wait(&sh.p_full[half], ph);
-        if (ok && elect_one()) at_mma_ts<D>(t_dv, t_s, do_mn + rb2.slot * ts, half, first);
+        if (ok) at_mma_ts<D>(t_dv, t_s, do_mn + rb2.slot * ts, half, first);
       }
       if (!ok) break;
-      if (elect_one()) umma_commit(&sh.b_empty[rb2.slot]);
+      umma_commit(&sh.b_empty[rb2.slot]);
       rb2.next();
       if (next && !scores(i + 1)) ok = false;
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         ok = ok && wait(&sh.ds_full[half], ph);
-        if (ok && elect_one()) at_mma_ts<D>(t_dk, t_dp, dq_mn + ra2.slot * ts, half, first);
+        if (ok) at_mma_ts<D>(t_dk, t_dp, dq_mn + ra2.slot * ts, half, first);
       }
       if (!ok) break;
-      if (elect_one()) {
-        umma_commit(&sh.a_empty[ra2.slot]);
-        umma_commit(&sh.st_empty[rs.slot]);
-        if (!next) umma_commit(&sh.acc_full);
-      }
+      umma_commit(&sh.a_empty[ra2.slot]);
+      umma_commit(&sh.st_empty[rs.slot]);
+      if (!next) umma_commit(&sh.acc_full);
       ra2.next();
       rs.next();
       ph ^= 1u;
       if (next && !dprobs(i + 1)) ok = false;
     }
     if (!ok) break;
+    if (x.ragged) zph ^= 1u;
   }
-  __syncwarp();
-  if (elect_one()) umma_commit(&sh.done);
+  umma_commit(&sh.done);
   mbar_wait<false>(&sh.done, 0u, wc);
+}
+
+// Rows behind the sequence's last query may be another sequence's, or hold anything: zeros, before the
+// products see them.  The loading thread asks for it with the tile's load; it is at most one unit ahead,
+// because the next unit's held tiles wait for this one's products.
+template <int D>
+__device__ __forceinline__ void at_dkv_ragged(AtBwdShared& sh, const AttnBwdArgs& a, uint8_t* smem_p, int64_t nu) {
+  using T = AtBwdTile<D>;
+  const WaitCtl wc{&sh.abort_flag, a.status, a.limit_ns};
+  AtRing<kAtSlotsA> ra;
+  AtRing<kAtSlotsB> rb;
+  uint32_t ph = 0;
+  for (int64_t r = 0, u; (u = at_turn(r)) < nu; ++r) {
+    const AtKvUnit x = at_kv_unit(a, u);
+    if (x.i0 >= x.i1) continue;
+    ra.skip(x.i1 - 1 - x.i0);
+    rb.skip(x.i1 - 1 - x.i0);
+    if (x.ragged) {
+      if (!at_wait(&sh.z_ask[0], ph, wc) || !at_wait(&sh.a_full[ra.slot], ra.phase, wc)) return;
+      at_zero_rows<D>(smem_p + T::ring_a + ra.slot * T::tile_bytes, x.rows);
+      if ((threadIdx.x & 31) == 0) mbar_arrive(&sh.z_full[0]);
+      if (!at_wait(&sh.z_ask[1], ph, wc) || !at_wait(&sh.b_full[rb.slot], rb.phase, wc)) return;
+      at_zero_rows<D>(smem_p + T::ring_b + rb.slot * T::tile_bytes, x.rows);
+      if ((threadIdx.x & 31) == 0) mbar_arrive(&sh.z_full[1]);
+      ph ^= 1u;
+    }
+    ra.next();
+    rb.next();
+  }
 }
 
 template <int D>
@@ -404,11 +437,7 @@ __device__ __forceinline__ void at_dkv_probs(AtBwdShared& sh, const AttnBwdArgs&
   uint32_t ph = 0, aph = 0;
   AtRing<2> rs;
   const float2 cc = make_float2(a.c, a.c);
-  auto wait = [&](uint64_t* bar, uint32_t parity) {
-    const bool ok = __all_sync(0xffffffffu, mbar_wait<false>(bar, parity, wc));
-    tc_fence_after();
-    return ok;
-  };
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return at_wait(bar, parity, wc); };
   for (int64_t r = 0, u; (u = at_turn(r)) < nu; ++r) {
     const AtKvUnit x = at_kv_unit(a, u);
     const int32_t key = x.t0 + key_in;
@@ -515,8 +544,11 @@ __global__ void __launch_bounds__(kAtBwdThreads, 1)
   } else if (warp == 8) {
     if (lane == 0) at_dkv_load<D>(sh, a, smem, nu, &mq, &mk, &mv, &mdo);
     __syncwarp();
+  } else if (warp == 9) {
+    if (elect_one()) at_dkv_mma<D>(sh, a, smem, nu, tmem);
+    __syncwarp();
   } else {
-    at_dkv_mma<D>(sh, a, dsmem, nu, tmem);
+    at_dkv_ragged<D>(sh, a, dsmem, nu);
   }
   at_bwd_end(sh, tmem);
 }
@@ -530,6 +562,8 @@ struct AtQUnit {
   AttnSeq q;
   int32_t h, t0;
   int32_t n;        // key tiles that a row of the unit sees
+  int32_t rows;     // keys of the last one
+  bool ragged;
 };
 __device__ __forceinline__ AtQUnit at_q_unit(const AttnBwdArgs& a, int64_t u) {
   AtQUnit x;
@@ -539,6 +573,8 @@ __device__ __forceinline__ AtQUnit at_q_unit(const AttnBwdArgs& a, int64_t u) {
   x.t0 = w.t0;
   const int32_t last = (w.t0 + a.tpt < x.q.lq ? w.t0 + a.tpt : x.q.lq) - 1;
   x.n = (attn_visible(last, x.q.lq, x.q.lk, a.causal) + kAtTile - 1) / kAtTile;
+  x.rows = x.q.lk - (x.n - 1) * kAtTile;
+  x.ragged = x.rows < kAtTile;
   return x;
 }
 
@@ -576,6 +612,7 @@ __device__ __forceinline__ void at_dq_load(AtBwdShared& sh, const AttnBwdArgs& a
         tma_load_3d(smem + T::ring_a + ra.slot * T::tile_bytes + b * kAUnitBytes, mk, &sh.a_full[ra.slot], b * 64, x.h,
                     static_cast<int32_t>(x.q.k0) + j * kAtTile);
       ra.next();
+      if (j + 1 == x.n && x.ragged) mbar_arrive(&sh.z_ask[0]);
       return true;
     };
     if (!key_tile(0)) return;
@@ -593,11 +630,10 @@ __device__ __forceinline__ void at_dq_load(AtBwdShared& sh, const AttnBwdArgs& a
 }
 
 template <int D>
-__device__ __forceinline__ void at_dq_mma(AtBwdShared& sh, const AttnBwdArgs& a, uint8_t* smem_p, int64_t nu,
+__device__ __forceinline__ void at_dq_mma(AtBwdShared& sh, const AttnBwdArgs& a, uint32_t smem, int64_t nu,
                                           uint32_t tmem) {
   using T = AtBwdTile<D>;
   const WaitCtl wc{&sh.abort_flag, a.status, a.limit_ns};
-  const uint32_t smem = smem_u32(smem_p);
   constexpr uint32_t ts = T::tile_bytes >> 4;
   const uint64_t dq = sdesc_k_sw128(smem), ddo = sdesc_k_sw128(smem + T::tile_bytes);
   const uint64_t dk_k = sdesc_k_sw128(smem + T::ring_a), dk_mn = sdesc_mn_sw128(smem + T::ring_a, kAUnitBytes);
@@ -606,9 +642,9 @@ __device__ __forceinline__ void at_dq_mma(AtBwdShared& sh, const AttnBwdArgs& a,
   AtRing<kAtSlotsA> ra, ra2;
   AtRing<kAtSlotsB> rb;
   AtRing<2> sb;                // score buffer of the next S
-  uint32_t hph = 0, ph = 0, cur = 0;
+  uint32_t hph = 0, ph = 0, cur = 0, zph = 0;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    const bool ok = __all_sync(0xffffffffu, mbar_wait<false>(bar, parity, wc));
+    const bool ok = mbar_wait<false>(bar, parity, wc);
     tc_fence_after();
     return ok;
   };
@@ -617,23 +653,18 @@ __device__ __forceinline__ void at_dq_mma(AtBwdShared& sh, const AttnBwdArgs& a,
     if (x.n == 0) continue;
     auto scores = [&](int32_t j) {
       if (!wait(&sh.a_full[ra.slot], ra.phase)) return false;
-      const int32_t rows = x.q.lk - j * kAtTile;
-      if (rows < kAtTile) at_zero_rows<D>(smem_p + T::ring_a + ra.slot * T::tile_bytes, rows);
-      if (elect_one()) {
-        at_mma_ss<D>(tmem + sb.slot * 128, dq, dk_k + ra.slot * ts);
-        umma_commit(&sh.s_full[sb.slot]);
-      }
+      if (j + 1 == x.n && x.ragged && !wait(&sh.z_full[0], zph)) return false;
+      at_mma_ss<D>(tmem + sb.slot * 128, dq, dk_k + ra.slot * ts);
+      umma_commit(&sh.s_full[sb.slot]);
       ra.next();
       sb.next();
       return true;
     };
     auto dprobs = [&](int32_t j) {
       if (!wait(&sh.b_full[rb.slot], rb.phase)) return false;
-      if (elect_one()) {
-        at_mma_ss<D>(t_dp, ddo, dv_k + rb.slot * ts);
-        umma_commit(&sh.dp_full);
-        umma_commit(&sh.b_empty[rb.slot]);
-      }
+      at_mma_ss<D>(t_dp, ddo, dv_k + rb.slot * ts);
+      umma_commit(&sh.dp_full);
+      umma_commit(&sh.b_empty[rb.slot]);
       rb.next();
       return true;
     };
@@ -641,7 +672,7 @@ __device__ __forceinline__ void at_dq_mma(AtBwdShared& sh, const AttnBwdArgs& a,
     hph ^= 1u;
     if (!scores(0) || !dprobs(0)) break;
     if (x.n > 1 && !scores(1)) break;
-    if (x.n == 1 && elect_one()) umma_commit(&sh.held_empty);
+    if (x.n == 1) umma_commit(&sh.held_empty);
     bool ok = true;
     for (int32_t j = 0; j < x.n && ok; ++j) {
       // One barrier for the whole tile: dP_{j+1} lets the next dS come, so nothing of this one may
@@ -649,25 +680,44 @@ __device__ __forceinline__ void at_dq_mma(AtBwdShared& sh, const AttnBwdArgs& a,
       if (!wait(&sh.ds_full[0], ph)) { ok = false; break; }
       if (j + 1 < x.n) {
         if (!dprobs(j + 1)) { ok = false; break; }
-        if (j + 2 == x.n && elect_one()) umma_commit(&sh.held_empty);
+        if (j + 2 == x.n) umma_commit(&sh.held_empty);
       }
-      if (elect_one()) {
 #pragma unroll
-        for (int half = 0; half < 2; ++half)
-          at_mma_ts<D>(t_dq, tmem + cur * 128, dk_mn + ra2.slot * ts, half, j == 0);
-        umma_commit(&sh.a_empty[ra2.slot]);
-        if (j + 1 == x.n) umma_commit(&sh.acc_full);
-      }
+      for (int half = 0; half < 2; ++half)
+        at_mma_ts<D>(t_dq, tmem + cur * 128, dk_mn + ra2.slot * ts, half, j == 0);
+      umma_commit(&sh.a_empty[ra2.slot]);
+      if (j + 1 == x.n) umma_commit(&sh.acc_full);
       ra2.next();
       cur ^= 1u;
       ph ^= 1u;
       if (j + 2 < x.n && !scores(j + 2)) ok = false;
     }
     if (!ok) break;
+    if (x.ragged) zph ^= 1u;
   }
-  __syncwarp();
-  if (elect_one()) umma_commit(&sh.done);
+  umma_commit(&sh.done);
   mbar_wait<false>(&sh.done, 0u, wc);
+}
+
+// The same for the keys behind a sequence's last one.
+template <int D>
+__device__ __forceinline__ void at_dq_ragged(AtBwdShared& sh, const AttnBwdArgs& a, uint8_t* smem_p, int64_t nu) {
+  using T = AtBwdTile<D>;
+  const WaitCtl wc{&sh.abort_flag, a.status, a.limit_ns};
+  AtRing<kAtSlotsA> ra;
+  uint32_t ph = 0;
+  for (int64_t r = 0, u; (u = at_turn(r)) < nu; ++r) {
+    const AtQUnit x = at_q_unit(a, u);
+    if (x.n == 0) continue;
+    ra.skip(x.n - 1);
+    if (x.ragged) {
+      if (!at_wait(&sh.z_ask[0], ph, wc) || !at_wait(&sh.a_full[ra.slot], ra.phase, wc)) return;
+      at_zero_rows<D>(smem_p + T::ring_a + ra.slot * T::tile_bytes, x.rows);
+      if ((threadIdx.x & 31) == 0) mbar_arrive(&sh.z_full[0]);
+      ph ^= 1u;
+    }
+    ra.next();
+  }
 }
 
 template <int D>
@@ -681,11 +731,7 @@ __device__ __forceinline__ void at_dq_probs(AtBwdShared& sh, const AttnBwdArgs& 
   uint32_t ph = 0, aph = 0;
   AtRing<2> sb;
   const float2 cc = make_float2(a.c, a.c);
-  auto wait = [&](uint64_t* bar, uint32_t parity) {
-    const bool ok = __all_sync(0xffffffffu, mbar_wait<false>(bar, parity, wc));
-    tc_fence_after();
-    return ok;
-  };
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return at_wait(bar, parity, wc); };
   for (int64_t r = 0, u; (u = at_turn(r)) < nu; ++r) {
     const AtQUnit x = at_q_unit(a, u);
     const int32_t tok = x.t0 + tok_in;
@@ -766,8 +812,11 @@ __global__ void __launch_bounds__(kAtBwdThreads, 1)
   } else if (warp == 8) {
     if (lane == 0) at_dq_load<D>(sh, a, smem, nu, &mq, &mk, &mv, &mdo);
     __syncwarp();
+  } else if (warp == 9) {
+    if (elect_one()) at_dq_mma<D>(sh, a, smem, nu, tmem);
+    __syncwarp();
   } else {
-    at_dq_mma<D>(sh, a, dsmem, nu, tmem);
+    at_dq_ragged<D>(sh, a, dsmem, nu);
   }
   at_bwd_end(sh, tmem);
 }
