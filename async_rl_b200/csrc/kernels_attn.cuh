@@ -273,6 +273,34 @@ __device__ __forceinline__ int64_t at_turn(int64_t r) {
 // Keeps a rarely taken branch a branch: its selects are not to be executed everywhere.
 __device__ __forceinline__ void at_rare() { asm volatile("" ::: "memory"); }
 
+// 2^x, x below 128: x = j + f with j the nearest whole number, 2^f by the polynomial of degree 4 whose
+// largest relative error on [-1/2, 1/2] is least (2^-18.5; found by Remez's exchange, the float32
+// coefficients below), times 2^j put together from j's bits.  -127 and less give 0, NaN stays NaN.
+__device__ __forceinline__ float2 ex2_poly(float2 x) {
+  constexpr float kMagic = 12582912.f + 127.f;  // 1.5 2^23: adding it rounds to a whole number, j + 127 in the low bits
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(x.x) : "f"(-127.f));
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(x.y) : "f"(-127.f));
+  const float2 t = add2(x, make_float2(kMagic, kMagic));
+  const float2 j = add2(t, make_float2(-kMagic, -kMagic));
+  const float2 f = fma2(j, make_float2(-1.f, -1.f), x);
+  float2 y = fma2(f, make_float2(0.009570102207362652f, 0.009570102207362652f),
+                  make_float2(0.05591785907745361f, 0.05591785907745361f));
+  y = fma2(y, f, make_float2(0.240247443318367f, 0.240247443318367f));
+  y = fma2(y, f, make_float2(0.6931217908859253f, 0.6931217908859253f));
+  y = fma2(y, f, make_float2(0.9999992847442627f, 0.9999992847442627f));
+  return mul2(y, make_float2(__uint_as_float(__float_as_uint(t.x) << 23), __uint_as_float(__float_as_uint(t.y) << 23)));
+}
+// 2^x of a pair of columns.  The special function unit gives 16 results a clock and SM, as long for a
+// tile's scores as its products take, so some columns of every 16 go to the FMA units instead; which
+// ones is a matter of the column alone, so a row's bits do not depend on its batch.
+#ifndef BI_AT_POLY
+#define BI_AT_POLY 0x94  // pairs 2, 4 and 7 of 8
+#endif
+__device__ __forceinline__ float2 at_ex2(int pair, float2 x) {
+  if ((BI_AT_POLY >> (pair % 8)) & 1) return ex2_poly(x);
+  return make_float2(ex2_approx(x.x), ex2_approx(x.y));
+}
+
 // A warp's wait for what MMAs left in tensor memory or what another role wrote.
 __device__ __forceinline__ bool at_wait(uint64_t* bar, uint32_t parity, const WaitCtl& wc) {
   const bool ok = __all_sync(0xffffffffu, mbar_wait<false>(bar, parity, wc));

@@ -93,7 +93,10 @@ __global__ void __launch_bounds__(kAtPreThreads) k_attn_pre(const AttnBwdArgs a)
 // ----------------------------------------------------------------------------------------------
 // shared by both kernels
 // ----------------------------------------------------------------------------------------------
-constexpr int kAtBwdThreads = 352;  // warps 0-7: p and ds; 8: TMA; 9: MMA; 10: ragged tiles
+// Warps 0-15: p and ds; 16: TMA; 17: MMA; 18: ragged tiles.  Four warps of each quarter of the SM hide one
+// another's latencies: with two of them, and 64 columns a thread, p took 1300 clocks a tile, not 900.
+constexpr int kAtBwdThreads = 608;
+constexpr int kAtBwdProbs = 16;
 constexpr int kAtSlotsA = 3, kAtSlotsB = 2;
 
 template <int D>
@@ -148,8 +151,8 @@ __device__ __forceinline__ uint32_t at_bwd_begin(AtBwdShared& sh) {
       mbar_init(&sh.z_full[i], 1);
       mbar_init(&sh.st_empty[i], 1);
       mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.p_full[i], 256);
-      mbar_init(&sh.ds_full[i], 256);
+      mbar_init(&sh.p_full[i], 32 * kAtBwdProbs);
+      mbar_init(&sh.ds_full[i], 32 * kAtBwdProbs);
     }
     mbar_init(&sh.dp_full, 1);
     mbar_init(&sh.acc_full, 1);
@@ -157,7 +160,7 @@ __device__ __forceinline__ uint32_t at_bwd_begin(AtBwdShared& sh) {
     sh.abort_flag = 0u;
     fence_mbar_init_cluster();
   }
-  if (threadIdx.x / 32 == 9) {
+  if (threadIdx.x / 32 == kAtBwdProbs + 1) {
     tmem_alloc(&sh.tmem_base, 512);
     tmem_relinquish();
   }
@@ -174,7 +177,7 @@ __device__ __forceinline__ void at_bwd_end(AtBwdShared& sh, uint32_t tmem) {
     while (globaltimer_ns() - t0 < 50000u) {
     }
   }
-  if (threadIdx.x / 32 == 9) {
+  if (threadIdx.x / 32 == kAtBwdProbs + 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
@@ -197,43 +200,43 @@ __device__ __forceinline__ void at_mma_ts(uint32_t d, uint32_t a, uint64_t db, i
   constexpr uint32_t idesc = idesc_bf16(128, D, false, true);
 #pragma unroll
   for (int k = 4 * half; k < 4 * half + 4; ++k)
-    umma_bf16_ta(d, a + (k / 2) * 32 + (k % 2) * 8, db + k * (2048 >> 4), idesc, (k > 0 || !first) ? 1u : 0u);
+    umma_bf16_ta(d, a + k * 16, db + k * (2048 >> 4), idesc, (k > 0 || !first) ? 1u : 0u);
 }
 
-// A thread's columns of a 128-column tile: 32 of each half, [half * 64 + X * 32, +32), X its group.
-// Its bf16 results go into the first 16 of the 32 columns that it read.
-__device__ __forceinline__ void at_get(uint32_t t, uint32_t (&s)[2][32]) {
-  tmem_ld32(t, s[0]);
-  tmem_ld32(t + 64, s[1]);
+// A thread's columns of a 128-column tile: 16 of each half, [half * 64 + X * 16, +16), X its group of four
+// warps.  Its bf16 results go into the first 8 of the 16 columns that it read.
+__device__ __forceinline__ void at_get(uint32_t t, uint32_t (&s)[2][16]) {
+  tmem_ld16(t, s[0]);
+  tmem_ld16(t + 64, s[1]);
   tmem_ld_wait();
-  tmem_ld_pin(s[0]);
-  tmem_ld_pin(s[1]);
+  tmem_ld_pin16(s[0]);
+  tmem_ld_pin16(s[1]);
 }
-__device__ __forceinline__ void at_put(uint32_t t, const float2 (&p)[16]) {
-  uint32_t w[16];
+__device__ __forceinline__ void at_put(uint32_t t, const float2 (&p)[8]) {
+  uint32_t w[8];
 #pragma unroll
-  for (int e = 0; e < 16; ++e) w[e] = pack_bf16x2(p[e].x, p[e].y);  // bf16: what the tensor cores take
-  tmem_st16(t, w);
+  for (int e = 0; e < 8; ++e) w[e] = pack_bf16x2(p[e].x, p[e].y);  // bf16: what the tensor cores take
+  tmem_st8(t, w);
 }
-// 32 columns of an accumulator, scaled, as bf16 (whole warp; stored where `valid`).
-__device__ __forceinline__ void at_store32(uint32_t t, float scale, uint16_t* o, bool valid) {
-  uint32_t s[32], w[16];
-  tmem_ld32(t, s);
+// 16 columns of an accumulator, scaled, as bf16 (whole warp; stored where `valid`).
+__device__ __forceinline__ void at_store16(uint32_t t, float scale, uint16_t* o, bool valid) {
+  uint32_t s[16], w[8];
+  tmem_ld16(t, s);
   tmem_ld_wait();
-  tmem_ld_pin(s);
+  tmem_ld_pin16(s);
 #pragma unroll
-  for (int e = 0; e < 16; ++e)
+  for (int e = 0; e < 8; ++e)
     w[e] = pack_bf16x2(__uint_as_float(s[2 * e]) * scale, __uint_as_float(s[2 * e + 1]) * scale);
   if (valid)
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
+    for (int e = 0; e < 2; ++e)
       reinterpret_cast<uint4*>(o)[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
 }
-__device__ __forceinline__ void at_zero32(uint16_t* o) {
+__device__ __forceinline__ void at_zero16(uint16_t* o) {
 #pragma unroll
-  for (int e = 0; e < 4; ++e) reinterpret_cast<uint4*>(o)[e] = make_uint4(0u, 0u, 0u, 0u);
+  for (int e = 0; e < 2; ++e) reinterpret_cast<uint4*>(o)[e] = make_uint4(0u, 0u, 0u, 0u);
 }
-__device__ __forceinline__ float2 at_pair(const uint32_t (&s)[32], int e) {
+__device__ __forceinline__ float2 at_pair(const uint32_t (&s)[16], int e) {
   return make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));
 }
 
@@ -373,9 +376,9 @@ __device__ __forceinline__ void at_dkv_mma(AtBwdShared& sh, const AttnBwdArgs& a
         if (ok) at_mma_ts<D>(t_dv, t_s, do_mn + rb2.slot * ts, half, first);
       }
       if (!ok) break;
+      if (next && !scores(i + 1)) ok = false;
       umma_commit(&sh.b_empty[rb2.slot]);
       rb2.next();
-      if (next && !scores(i + 1)) ok = false;
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         ok = ok && wait(&sh.ds_full[half], ph);
@@ -432,8 +435,9 @@ __device__ __forceinline__ void at_dkv_probs(AtBwdShared& sh, const AttnBwdArgs&
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int X = warp >> 2, key_in = (warp & 3) * 32 + lane;
   const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-  const uint32_t t_s = tmem + lanes + X * 32, t_dp = t_s + 128;
-  const uint32_t t_acc = tmem + lanes + 256 + (X == 0 ? D : 0);  // group 0 stores dK, group 1 dV
+  const uint32_t t_s = tmem + lanes + X * 16, t_dp = t_s + 128;
+  const int part = (X & 1) * (D / 2);  // groups 0 and 1 store a half of dK each, 2 and 3 of dV
+  const uint32_t t_acc = tmem + lanes + 256 + (X < 2 ? D : 0) + part;
   uint32_t ph = 0, aph = 0;
   AtRing<2> rs;
   const float2 cc = make_float2(a.c, a.c);
@@ -442,11 +446,11 @@ __device__ __forceinline__ void at_dkv_probs(AtBwdShared& sh, const AttnBwdArgs&
     const AtKvUnit x = at_kv_unit(a, u);
     const int32_t key = x.t0 + key_in;
     const bool valid = key < x.q.lk;
-    uint16_t* o = X == 0 ? a.o0 + (x.q.k0 + key) * a.ld0 + x.h * D : a.o1 + (x.q.k0 + key) * a.ld1 + x.h * D;
+    uint16_t* o = (X < 2 ? a.o0 + (x.q.k0 + key) * a.ld0 : a.o1 + (x.q.k0 + key) * a.ld1) + x.h * D + part;
     if (x.i0 >= x.i1) {  // no query sees these keys
       if (valid)
 #pragma unroll
-        for (int b = 0; b < D / 32; ++b) at_zero32(o + b * 32);
+        for (int b = 0; b < D / 32; ++b) at_zero16(o + b * 16);
       continue;
     }
     // this key's first query
@@ -458,26 +462,26 @@ __device__ __forceinline__ void at_dkv_probs(AtBwdShared& sh, const AttnBwdArgs&
       const bool masked = __any_sync(0xffffffffu, low > 0);
       if (!wait(&sh.st_full[rs.slot], rs.phase)) return;
       if (!wait(&sh.s_full[0], ph)) return;
-      const float4* nl = reinterpret_cast<const float4*>(&sh.st[rs.slot][0][X * 32]);
-      const float4* nd = reinterpret_cast<const float4*>(&sh.st[rs.slot][1][X * 32]);
-      uint32_t s[2][32];
-      float2 p[2][16];
+      const float4* nl = reinterpret_cast<const float4*>(&sh.st[rs.slot][0][X * 16]);
+      const float4* nd = reinterpret_cast<const float4*>(&sh.st[rs.slot][1][X * 16]);
+      uint32_t s[2][16];
+      float2 p[2][8];
       at_get(t_s, s);
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         if (masked) {
           at_rare();
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (half * 64 + X * 32 + e < low) s[half][e] = 0xff800000u;  // -inf
+          for (int e = 0; e < 16; ++e)
+            if (half * 64 + X * 16 + e < low) s[half][e] = 0xff800000u;  // -inf
         }
 #pragma unroll
-        for (int e = 0; e < 16; e += 2) {
+        for (int e = 0; e < 8; e += 2) {
           const float4 l = nl[half * 16 + e / 2];
           const float2 y0 = fma2(at_pair(s[half], e), cc, make_float2(l.x, l.y));
           const float2 y1 = fma2(at_pair(s[half], e + 1), cc, make_float2(l.z, l.w));
-          p[half][e] = make_float2(ex2_approx(y0.x), ex2_approx(y0.y));
-          p[half][e + 1] = make_float2(ex2_approx(y1.x), ex2_approx(y1.y));
+          p[half][e] = at_ex2(e, y0);
+          p[half][e + 1] = at_ex2(e + 1, y1);
         }
         at_put(t_s + half * 64, p[half]);
         tmem_st_wait();
@@ -491,11 +495,11 @@ __device__ __forceinline__ void at_dkv_probs(AtBwdShared& sh, const AttnBwdArgs&
         if (masked) {
           at_rare();
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (half * 64 + X * 32 + e < low) s[half][e] = 0u;  // p is 0 there; what v holds does not matter
+          for (int e = 0; e < 16; ++e)
+            if (half * 64 + X * 16 + e < low) s[half][e] = 0u;  // p is 0 there; what v holds does not matter
         }
 #pragma unroll
-        for (int e = 0; e < 16; e += 2) {
+        for (int e = 0; e < 8; e += 2) {
           const float4 d = nd[half * 16 + e / 2];
           p[half][e] = mul2(p[half][e], add2(at_pair(s[half], e), make_float2(d.x, d.y)));
           p[half][e + 1] = mul2(p[half][e + 1], add2(at_pair(s[half], e + 1), make_float2(d.z, d.w)));
@@ -511,7 +515,7 @@ __device__ __forceinline__ void at_dkv_probs(AtBwdShared& sh, const AttnBwdArgs&
     if (!wait(&sh.acc_full, aph)) return;
     aph ^= 1u;
 #pragma unroll 1
-    for (int b = 0; b < D / 32; ++b) at_store32(t_acc + b * 32, X == 0 ? a.scale : 1.f, o + b * 32, valid);
+    for (int b = 0; b < D / 32; ++b) at_store16(t_acc + b * 16, X < 2 ? a.scale : 1.f, o + b * 16, valid);
   }
 }
 
@@ -539,12 +543,12 @@ __global__ void __launch_bounds__(kAtBwdThreads, 1)
   if (misaligned && threadIdx.x == 0) raise_status(a.status, 4 /* BI_ERR_CUDA */);
   const int64_t nu = misaligned ? 0 : static_cast<int64_t>(a.head->nunits) * a.Hkv;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (warp < 8) {
+  if (warp < kAtBwdProbs) {
     at_dkv_probs<D>(sh, a, nu, tmem);
-  } else if (warp == 8) {
+  } else if (warp == kAtBwdProbs) {
     if (lane == 0) at_dkv_load<D>(sh, a, smem, nu, &mq, &mk, &mv, &mdo);
     __syncwarp();
-  } else if (warp == 9) {
+  } else if (warp == kAtBwdProbs + 1) {
     if (elect_one()) at_dkv_mma<D>(sh, a, smem, nu, tmem);
     __syncwarp();
   } else {
@@ -727,7 +731,7 @@ __device__ __forceinline__ void at_dq_probs(AtBwdShared& sh, const AttnBwdArgs& 
   const int X = warp >> 2, row = (warp & 3) * 32 + lane;
   const int tok_in = row / a.G, g = row - tok_in * a.G;
   const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-  const uint32_t t_s = tmem + lanes + X * 32, t_dp = t_s + 256;
+  const uint32_t t_s = tmem + lanes + X * 16, t_dp = t_s + 256;
   uint32_t ph = 0, aph = 0;
   AtRing<2> sb;
   const float2 cc = make_float2(a.c, a.c);
@@ -737,11 +741,11 @@ __device__ __forceinline__ void at_dq_probs(AtBwdShared& sh, const AttnBwdArgs& 
     const int32_t tok = x.t0 + tok_in;
     const bool valid = tok_in < a.tpt && tok < x.q.lq;
     const int32_t vis = valid ? attn_visible(tok, x.q.lq, x.q.lk, a.causal) : 0;
-    uint16_t* o = a.o0 + (x.q.q0 + tok) * a.ld0 + static_cast<int64_t>(x.h * a.G + g) * D + X * (D / 2);
+    uint16_t* o = a.o0 + (x.q.q0 + tok) * a.ld0 + static_cast<int64_t>(x.h * a.G + g) * D + X * (D / 4);
     if (x.n == 0) {  // no key to see
       if (valid)
 #pragma unroll
-        for (int b = 0; b < D / 64; ++b) at_zero32(o + b * 32);
+        for (int b = 0; b < D / 64; ++b) at_zero16(o + b * 16);
       continue;
     }
     const float* st = a.st + (x.h * a.tiles + x.q.unit0 + x.t0 / a.tpt) * (2 * kAtTile) + row;
@@ -750,21 +754,20 @@ __device__ __forceinline__ void at_dq_probs(AtBwdShared& sh, const AttnBwdArgs& 
       const int32_t lim = vis - j * kAtTile;  // columns from here on are not seen
       const bool masked = __any_sync(0xffffffffu, lim < kAtTile);
       if (!wait(&sh.s_full[sb.slot], sb.phase)) return;
-      uint32_t s[2][32];
-      float2 p[2][16];
+      uint32_t s[2][16];
+      float2 p[2][8];
       at_get(t_s + sb.slot * 128, s);
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         if (masked) {
           at_rare();
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (half * 64 + X * 32 + e >= lim) s[half][e] = 0xff800000u;  // -inf
+          for (int e = 0; e < 16; ++e)
+            if (half * 64 + X * 16 + e >= lim) s[half][e] = 0xff800000u;  // -inf
         }
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const float2 y = fma2(at_pair(s[half], e), cc, nl);
-          p[half][e] = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+        for (int e = 0; e < 8; ++e) {
+          p[half][e] = at_ex2(e, fma2(at_pair(s[half], e), cc, nl));
         }
       }
       if (!wait(&sh.dp_full, ph)) return;
@@ -774,11 +777,11 @@ __device__ __forceinline__ void at_dq_probs(AtBwdShared& sh, const AttnBwdArgs& 
         if (masked) {
           at_rare();
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (half * 64 + X * 32 + e >= lim) s[half][e] = 0u;  // what v holds there does not matter
+          for (int e = 0; e < 16; ++e)
+            if (half * 64 + X * 16 + e >= lim) s[half][e] = 0u;  // what v holds there does not matter
         }
 #pragma unroll
-        for (int e = 0; e < 16; ++e) p[half][e] = mul2(p[half][e], add2(at_pair(s[half], e), nd));
+        for (int e = 0; e < 8; ++e) p[half][e] = mul2(p[half][e], add2(at_pair(s[half], e), nd));
         at_put(t_s + sb.slot * 128 + half * 64, p[half]);
       }
       tmem_st_wait();
@@ -789,9 +792,9 @@ __device__ __forceinline__ void at_dq_probs(AtBwdShared& sh, const AttnBwdArgs& 
     }
     if (!wait(&sh.acc_full, aph)) return;
     aph ^= 1u;
-#pragma unroll 1
+#pragma unroll
     for (int b = 0; b < D / 64; ++b)
-      at_store32(tmem + lanes + 384 + X * (D / 2) + b * 32, a.scale, o + b * 32, valid);
+      at_store16(tmem + lanes + 384 + X * (D / 4) + b * 16, a.scale, o + b * 16, valid);
   }
 }
 
@@ -807,12 +810,12 @@ __global__ void __launch_bounds__(kAtBwdThreads, 1)
   if (misaligned && threadIdx.x == 0) raise_status(a.status, 4 /* BI_ERR_CUDA */);
   const int64_t nu = misaligned ? 0 : static_cast<int64_t>(a.head->nunits) * a.Hkv;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (warp < 8) {
+  if (warp < kAtBwdProbs) {
     at_dq_probs<D>(sh, a, nu, tmem);
-  } else if (warp == 8) {
+  } else if (warp == kAtBwdProbs) {
     if (lane == 0) at_dq_load<D>(sh, a, smem, nu, &mq, &mk, &mv, &mdo);
     __syncwarp();
-  } else if (warp == 9) {
+  } else if (warp == kAtBwdProbs + 1) {
     if (elect_one()) at_dq_mma<D>(sh, a, smem, nu, tmem);
     __syncwarp();
   } else {
