@@ -493,7 +493,8 @@ __device__ __forceinline__ void at_fwd_softmax(AtFwdShared& sh, const AttnFwdArg
     const int32_t tok = x.t0 + X * a.tpt + tok_in;
     const bool valid = tok_in < a.tpt && tok < x.q.lq;
     const bool warp_valid = __any_sync(0xffffffffu, valid);
-    const int32_t vis = valid ? attn_visible(tok, x.q.lq, x.q.lk, a.causal) : 0;
+    // rows without a query see all, so that they do not make their warp mask every tile
+    const int32_t vis = valid ? attn_visible(tok, x.q.lq, x.q.lk, a.causal) : 0x7fffffff;
     const int32_t head = x.h * a.G + g;
     uint16_t* out = a.out + ((x.q.q0 + tok) * a.Hq + head) * D;
     float* lse = a.lse + static_cast<int64_t>(head) * a.Tq + x.q.q0 + tok;

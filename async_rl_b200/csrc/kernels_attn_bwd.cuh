@@ -108,7 +108,7 @@ struct AtBwdTile {
 };
 struct AtBwdShared {
   float st[2][2][kAtTile];
-  uint64_t held_full, held_empty;
+  uint64_t held_full[2], held_empty[2];
   uint64_t a_full[kAtSlotsA], a_empty[kAtSlotsA];
   uint64_t b_full[kAtSlotsB], b_empty[kAtSlotsB];
   uint64_t st_full[2], st_empty[2];
@@ -132,11 +132,44 @@ struct AtRing {
   }
 };
 
+// The tiles of a CTA's units one behind another.  The next unit's description is fetched a unit ahead,
+// so that nothing waits for it at the turn.
+struct AtStep {
+  bool first, last, ragged;  // first and last tile of its unit; that has rows to clear
+};
+template <class Unit>
+struct AtWalk {
+  const AttnBwdArgs& a;
+  const int64_t nu;
+  int64_t r = 0;
+  Unit x, nx;           // the current unit and the next one
+  int32_t i = 0, n = 0;  // of its tiles
+  bool more;
+  __device__ __forceinline__ AtWalk(const AttnBwdArgs& args, int64_t units) : a(args), nu(units) {
+    more = at_turn(0) < nu;
+    if (more) nx.fetch(a, at_turn(0));
+  }
+  __device__ __forceinline__ bool step(AtStep& s) {
+    while (i == n) {
+      if (!more) return false;
+      x = nx;
+      i = 0;
+      n = x.tiles();
+      const int64_t u = at_turn(++r);
+      more = u < nu;
+      if (more) nx.fetch(a, u);
+    }
+    s.first = i == 0;
+    ++i;
+    s.last = i == n;
+    s.ragged = s.last && x.ragged;
+    return true;
+  }
+};
+
 // Warp roles' common start and end; returns the base of tensor memory.
 __device__ __forceinline__ uint32_t at_bwd_begin(AtBwdShared& sh) {
   if (threadIdx.x == 0) {
-    mbar_init(&sh.held_full, 1);
-    mbar_init(&sh.held_empty, 1);
     for (int i = 0; i < kAtSlotsA; ++i) {
       mbar_init(&sh.a_full[i], 1);
       mbar_init(&sh.a_empty[i], 1);
@@ -147,6 +180,8 @@ __device__ __forceinline__ uint32_t at_bwd_begin(AtBwdShared& sh) {
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.st_full[i], 1);
+      mbar_init(&sh.held_full[i], 1);
+      mbar_init(&sh.held_empty[i], 1);
       mbar_init(&sh.z_ask[i], 1);
       mbar_init(&sh.z_full[i], 1);
       mbar_init(&sh.st_empty[i], 1);
@@ -254,21 +289,20 @@ struct AtKvUnit {
   int64_t tile0;    // of the sequence's first query tile
   int32_t rows;     // of the last query tile
   bool ragged;
+  __device__ __forceinline__ int32_t tiles() const { return i1 - i0; }
+  __device__ __forceinline__ void fetch(const AttnBwdArgs& a, int64_t u) {
+    const AttnUnit w = a.units[u / a.Hkv];
+    h = static_cast<int32_t>(u % a.Hkv);
+    q = a.seqs[w.seq];
+    t0 = w.t0;
+    const int32_t first = attn_first_query(t0, q.lq, q.lk, a.causal);
+    i1 = (q.lq + a.tpt - 1) / a.tpt;
+    i0 = first >= q.lq ? i1 : first / a.tpt;
+    tile0 = a.rows[w.seq].unit0;
+    rows = (q.lq - (i1 - 1) * a.tpt) * a.G;
+    ragged = rows < a.tpt * a.G;
+  }
 };
-__device__ __forceinline__ AtKvUnit at_kv_unit(const AttnBwdArgs& a, int64_t u) {
-  AtKvUnit x;
-  const AttnUnit w = a.units[u / a.Hkv];
-  x.h = static_cast<int32_t>(u % a.Hkv);
-  x.q = a.seqs[w.seq];
-  x.t0 = w.t0;
-  const int32_t first = attn_first_query(w.t0, x.q.lq, x.q.lk, a.causal);
-  x.i1 = (x.q.lq + a.tpt - 1) / a.tpt;
-  x.i0 = first >= x.q.lq ? x.i1 : first / a.tpt;
-  x.tile0 = a.rows[w.seq].unit0;
-  x.rows = (x.q.lq - (x.i1 - 1) * a.tpt) * a.G;
-  x.ragged = x.rows < a.tpt * a.G;
-  return x;
-}
 
 template <int D>
 __device__ __forceinline__ void at_dkv_load(AtBwdShared& sh, const AttnBwdArgs& a, uint32_t smem, int64_t nu,
@@ -285,43 +319,47 @@ __device__ __forceinline__ void at_dkv_load(AtBwdShared& sh, const AttnBwdArgs& 
   AtRing<kAtSlotsB> rb;
   AtRing<2> rs;
   uint32_t hph = 0;
-  for (int64_t r = 0, u; (u = at_turn(r)) < nu; ++r) {
-    const AtKvUnit x = at_kv_unit(a, u);
-    if (x.i0 >= x.i1) continue;
-    if (!mbar_wait<false>(&sh.held_empty, hph ^ 1u, wc)) return;
-    hph ^= 1u;
-    mbar_arrive_expect_tx(&sh.held_full, 2 * T::tile_bytes);
-    const int32_t key = static_cast<int32_t>(x.q.k0) + x.t0;
+  AtWalk<AtKvUnit> walk(a, nu);
+  AtStep f;
+  auto held = [&](int w, const CUtensorMap* m) {
+    if (!mbar_wait<false>(&sh.held_empty[w], hph ^ 1u, wc)) return false;
+    mbar_arrive_expect_tx(&sh.held_full[w], T::tile_bytes);
 #pragma unroll
-    for (int b = 0; b < D / 64; ++b) {
-      tma_load_3d(smem + b * kAUnitBytes, mk, &sh.held_full, b * 64, x.h, key);
-      tma_load_3d(smem + T::tile_bytes + b * kAUnitBytes, mv, &sh.held_full, b * 64, x.h, key);
+    for (int b = 0; b < D / 64; ++b)
+      tma_load_3d(smem + w * T::tile_bytes + b * kAUnitBytes, m, &sh.held_full[w], b * 64, walk.x.h,
+                  static_cast<int32_t>(walk.x.q.k0) + walk.x.t0);
+    return true;
+  };
+  while (walk.step(f)) {
+    const AtKvUnit& x = walk.x;
+    const int32_t i = x.i0 + walk.i - 1;
+    const int32_t row = static_cast<int32_t>(x.q.q0) + i * a.tpt;
+    if (f.first && !held(0, mk)) return;
+    if (!mbar_wait<false>(&sh.a_empty[ra.slot], ra.phase ^ 1u, wc)) return;
+    mbar_arrive_expect_tx(&sh.a_full[ra.slot], bytes);
+#pragma unroll
+    for (int b = 0; b < D / 64; ++b)
+      tma_load_3d(smem + T::ring_a + ra.slot * T::tile_bytes + b * kAUnitBytes, mq, &sh.a_full[ra.slot], b * 64,
+                  x.h * a.G, row);
+    ra.next();
+    if (f.ragged) mbar_arrive(&sh.z_ask[0]);
+    if (!mbar_wait<false>(&sh.st_empty[rs.slot], rs.phase ^ 1u, wc)) return;
+    mbar_arrive_expect_tx(&sh.st_full[rs.slot], 2 * kAtTile * 4);
+    bulk_load(smem_u32(&sh.st[rs.slot][0][0]), a.st + (x.h * a.tiles + x.tile0 + i) * (2 * kAtTile), 2 * kAtTile * 4,
+              &sh.st_full[rs.slot]);
+    rs.next();
+    if (f.first) {
+      if (!held(1, mv)) return;
+      hph ^= 1u;
     }
-    const float* st = a.st + (x.h * a.tiles + x.tile0) * (2 * kAtTile);
-    for (int32_t i = x.i0; i < x.i1; ++i) {
-      const int32_t row = static_cast<int32_t>(x.q.q0) + i * a.tpt;
-      if (!mbar_wait<false>(&sh.a_empty[ra.slot], ra.phase ^ 1u, wc)) return;
-      mbar_arrive_expect_tx(&sh.a_full[ra.slot], bytes);
+    if (!mbar_wait<false>(&sh.b_empty[rb.slot], rb.phase ^ 1u, wc)) return;
+    mbar_arrive_expect_tx(&sh.b_full[rb.slot], bytes);
 #pragma unroll
-      for (int b = 0; b < D / 64; ++b)
-        tma_load_3d(smem + T::ring_a + ra.slot * T::tile_bytes + b * kAUnitBytes, mq, &sh.a_full[ra.slot], b * 64,
-                    x.h * a.G, row);
-      ra.next();
-      if (i + 1 == x.i1 && x.ragged) mbar_arrive(&sh.z_ask[0]);
-      if (!mbar_wait<false>(&sh.st_empty[rs.slot], rs.phase ^ 1u, wc)) return;
-      mbar_arrive_expect_tx(&sh.st_full[rs.slot], 2 * kAtTile * 4);
-      bulk_load(smem_u32(&sh.st[rs.slot][0][0]), st + static_cast<int64_t>(i) * (2 * kAtTile), 2 * kAtTile * 4,
-                &sh.st_full[rs.slot]);
-      rs.next();
-      if (!mbar_wait<false>(&sh.b_empty[rb.slot], rb.phase ^ 1u, wc)) return;
-      mbar_arrive_expect_tx(&sh.b_full[rb.slot], bytes);
-#pragma unroll
-      for (int b = 0; b < D / 64; ++b)
-        tma_load_3d(smem + T::ring_b + rb.slot * T::tile_bytes + b * kAUnitBytes, mdo, &sh.b_full[rb.slot], b * 64,
-                    x.h * a.G, row);
-      rb.next();
-      if (i + 1 == x.i1 && x.ragged) mbar_arrive(&sh.z_ask[1]);
-    }
+    for (int b = 0; b < D / 64; ++b)
+      tma_load_3d(smem + T::ring_b + rb.slot * T::tile_bytes + b * kAUnitBytes, mdo, &sh.b_full[rb.slot], b * 64,
+                  x.h * a.G, row);
+    rb.next();
+    if (f.ragged) mbar_arrive(&sh.z_ask[1]);
   }
 }
 
@@ -338,71 +376,75 @@ __device__ __forceinline__ void at_dkv_mma(AtBwdShared& sh, const AttnBwdArgs& a
   AtRing<kAtSlotsA> ra, ra2;  // next tile to arrive, tile whose dK is next
   AtRing<kAtSlotsB> rb, rb2;
   AtRing<2> rs;
-  uint32_t hph = 0, ph = 0, zph = 0;
+  uint32_t hph[2] = {0, 0}, zph[2] = {0, 0}, ph = 0;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     const bool ok = mbar_wait<false>(bar, parity, wc);
     tc_fence_after();
     return ok;
   };
-  for (int64_t r = 0, u; (u = at_turn(r)) < nu; ++r) {
-    const AtKvUnit x = at_kv_unit(a, u);
-    if (x.i0 >= x.i1) continue;
-    auto scores = [&](int32_t i) {
-      if (!wait(&sh.a_full[ra.slot], ra.phase)) return false;
-      if (i + 1 == x.i1 && x.ragged && !wait(&sh.z_full[0], zph)) return false;
-      at_mma_ss<D>(t_s, dk, dq_k + ra.slot * ts);
-      umma_commit(&sh.s_full[0]);
-      ra.next();
-      return true;
-    };
-    auto dprobs = [&](int32_t i) {
-      if (!wait(&sh.b_full[rb.slot], rb.phase)) return false;
-      if (i + 1 == x.i1 && x.ragged && !wait(&sh.z_full[1], zph)) return false;
-      at_mma_ss<D>(t_dp, dv, do_k + rb.slot * ts);
-      umma_commit(&sh.dp_full);
-      if (i + 1 == x.i1) umma_commit(&sh.held_empty);
-      rb.next();
-      return true;
-    };
-    if (!wait(&sh.held_full, hph)) break;
-    hph ^= 1u;
-    if (!scores(x.i0) || !dprobs(x.i0)) break;
-    bool ok = true;
-    for (int32_t i = x.i0; i < x.i1 && ok; ++i) {
-      const bool first = i == x.i0, next = i + 1 < x.i1;
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        ok = ok && wait(&sh.p_full[half], ph);
-        if (ok) at_mma_ts<D>(t_dv, t_s, do_mn + rb2.slot * ts, half, first);
-      }
-      if (!ok) break;
-      if (next && !scores(i + 1)) ok = false;
-      umma_commit(&sh.b_empty[rb2.slot]);
-      rb2.next();
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        ok = ok && wait(&sh.ds_full[half], ph);
-        if (ok) at_mma_ts<D>(t_dk, t_dp, dq_mn + ra2.slot * ts, half, first);
-      }
-      if (!ok) break;
-      umma_commit(&sh.a_empty[ra2.slot]);
-      umma_commit(&sh.st_empty[rs.slot]);
-      if (!next) umma_commit(&sh.acc_full);
-      ra2.next();
-      rs.next();
-      ph ^= 1u;
-      if (next && !dprobs(i + 1)) ok = false;
+  // a new unit's held tile, and the zeros of a ragged one
+  auto ready = [&](int w, const AtStep& f) {
+    if (f.first) {
+      if (!wait(&sh.held_full[w], hph[w])) return false;
+      hph[w] ^= 1u;
     }
-    if (!ok) break;
-    if (x.ragged) zph ^= 1u;
+    if (f.ragged) {
+      if (!wait(&sh.z_full[w], zph[w])) return false;
+      zph[w] ^= 1u;
+    }
+    return true;
+  };
+  auto scores = [&](const AtStep& f) {
+    if (!wait(&sh.a_full[ra.slot], ra.phase) || !ready(0, f)) return false;
+    at_mma_ss<D>(t_s, dk, dq_k + ra.slot * ts);
+    umma_commit(&sh.s_full[0]);
+    if (f.last) umma_commit(&sh.held_empty[0]);
+    ra.next();
+    return true;
+  };
+  auto dprobs = [&](const AtStep& f) {
+    if (!wait(&sh.b_full[rb.slot], rb.phase) || !ready(1, f)) return false;
+    at_mma_ss<D>(t_dp, dv, do_k + rb.slot * ts);
+    umma_commit(&sh.dp_full);
+    if (f.last) umma_commit(&sh.held_empty[1]);
+    rb.next();
+    return true;
+  };
+  AtWalk<AtKvUnit> walk(a, nu);
+  AtStep f, fn;
+  bool go = walk.step(f) && scores(f) && dprobs(f);
+  while (go) {
+    const bool next = walk.step(fn);
+#pragma unroll
+    for (int half = 0; half < 2 && go; ++half) {
+      go = wait(&sh.p_full[half], ph);
+      if (go) at_mma_ts<D>(t_dv, t_s, do_mn + rb2.slot * ts, half, f.first);
+    }
+    if (!go || (next && !scores(fn))) break;
+    umma_commit(&sh.b_empty[rb2.slot]);
+    rb2.next();
+#pragma unroll
+    for (int half = 0; half < 2 && go; ++half) {
+      go = wait(&sh.ds_full[half], ph);
+      if (go) at_mma_ts<D>(t_dk, t_dp, dq_mn + ra2.slot * ts, half, f.first);
+    }
+    if (!go) break;
+    umma_commit(&sh.a_empty[ra2.slot]);
+    umma_commit(&sh.st_empty[rs.slot]);
+    if (f.last) umma_commit(&sh.acc_full);
+    ra2.next();
+    rs.next();
+    ph ^= 1u;
+    go = next && dprobs(fn);
+    f = fn;
   }
   umma_commit(&sh.done);
   mbar_wait<false>(&sh.done, 0u, wc);
 }
 
 // Rows behind the sequence's last query may be another sequence's, or hold anything: zeros, before the
-// products see them.  The loading thread asks for it with the tile's load; it is at most one unit ahead,
-// because the next unit's held tiles wait for this one's products.
+// products see them.  The loading thread asks for it with the tile's load; it is never two units ahead,
+// because a unit's held tiles wait for the products with the last tiles of the unit before.
 template <int D>
 __device__ __forceinline__ void at_dkv_ragged(AtBwdShared& sh, const AttnBwdArgs& a, uint8_t* smem_p, int64_t nu) {
   using T = AtBwdTile<D>;
@@ -411,7 +453,8 @@ __device__ __forceinline__ void at_dkv_ragged(AtBwdShared& sh, const AttnBwdArgs
   AtRing<kAtSlotsB> rb;
   uint32_t ph = 0;
   for (int64_t r = 0, u; (u = at_turn(r)) < nu; ++r) {
-    const AtKvUnit x = at_kv_unit(a, u);
+    AtKvUnit x;
+    x.fetch(a, u);
     if (x.i0 >= x.i1) continue;
     ra.skip(x.i1 - 1 - x.i0);
     rb.skip(x.i1 - 1 - x.i0);
@@ -442,8 +485,20 @@ __device__ __forceinline__ void at_dkv_probs(AtBwdShared& sh, const AttnBwdArgs&
   AtRing<2> rs;
   const float2 cc = make_float2(a.c, a.c);
   auto wait = [&](uint64_t* bar, uint32_t parity) { return at_wait(bar, parity, wc); };
+  // A unit's sums are stored when the next unit's first p is computed: its scores are there by then.
+  uint16_t* done_o = nullptr;
+  bool done_valid = false, pending = false;
+  auto store = [&]() {
+    if (!wait(&sh.acc_full, aph)) return false;
+    aph ^= 1u;
+#pragma unroll 1
+    for (int b = 0; b < D / 32; ++b) at_store16(t_acc + b * 16, X < 2 ? a.scale : 1.f, done_o + b * 16, done_valid);
+    pending = false;
+    return true;
+  };
   for (int64_t r = 0, u; (u = at_turn(r)) < nu; ++r) {
-    const AtKvUnit x = at_kv_unit(a, u);
+    AtKvUnit x;
+    x.fetch(a, u);
     const int32_t key = x.t0 + key_in;
     const bool valid = key < x.q.lk;
     uint16_t* o = (X < 2 ? a.o0 + (x.q.k0 + key) * a.ld0 : a.o1 + (x.q.k0 + key) * a.ld1) + x.h * D + part;
@@ -483,6 +538,7 @@ __device__ __forceinline__ void at_dkv_probs(AtBwdShared& sh, const AttnBwdArgs&
           p[half][e] = at_ex2(e, y0);
           p[half][e + 1] = at_ex2(e + 1, y1);
         }
+        if (pending && !store()) return;
         at_put(t_s + half * 64, p[half]);
         tmem_st_wait();
         tc_fence_before();
@@ -512,11 +568,11 @@ __device__ __forceinline__ void at_dkv_probs(AtBwdShared& sh, const AttnBwdArgs&
       rs.next();
       ph ^= 1u;
     }
-    if (!wait(&sh.acc_full, aph)) return;
-    aph ^= 1u;
-#pragma unroll 1
-    for (int b = 0; b < D / 32; ++b) at_store16(t_acc + b * 16, X < 2 ? a.scale : 1.f, o + b * 16, valid);
+    pending = true;
+    done_o = o;
+    done_valid = valid;
   }
+  if (pending) store();
 }
 
 // Rows [tpt G, 128) of every query tile are never loaded: zeros from the start.
@@ -568,19 +624,18 @@ struct AtQUnit {
   int32_t n;        // key tiles that a row of the unit sees
   int32_t rows;     // keys of the last one
   bool ragged;
+  __device__ __forceinline__ int32_t tiles() const { return n; }
+  __device__ __forceinline__ void fetch(const AttnBwdArgs& a, int64_t u) {
+    const AttnUnit w = a.units[u / a.Hkv];
+    h = static_cast<int32_t>(u % a.Hkv);
+    q = a.seqs[w.seq];
+    t0 = w.t0;
+    const int32_t last = (t0 + a.tpt < q.lq ? t0 + a.tpt : q.lq) - 1;
+    n = (attn_visible(last, q.lq, q.lk, a.causal) + kAtTile - 1) / kAtTile;
+    rows = q.lk - (n - 1) * kAtTile;
+    ragged = rows < kAtTile;
+  }
 };
-__device__ __forceinline__ AtQUnit at_q_unit(const AttnBwdArgs& a, int64_t u) {
-  AtQUnit x;
-  const AttnUnit w = a.units[u / a.Hkv];
-  x.h = static_cast<int32_t>(u % a.Hkv);
-  x.q = a.seqs[w.seq];
-  x.t0 = w.t0;
-  const int32_t last = (w.t0 + a.tpt < x.q.lq ? w.t0 + a.tpt : x.q.lq) - 1;
-  x.n = (attn_visible(last, x.q.lq, x.q.lk, a.causal) + kAtTile - 1) / kAtTile;
-  x.rows = x.q.lk - (x.n - 1) * kAtTile;
-  x.ragged = x.rows < kAtTile;
-  return x;
-}
 
 template <int D>
 __device__ __forceinline__ void at_dq_load(AtBwdShared& sh, const AttnBwdArgs& a, uint32_t smem, int64_t nu,
@@ -596,40 +651,38 @@ __device__ __forceinline__ void at_dq_load(AtBwdShared& sh, const AttnBwdArgs& a
   AtRing<kAtSlotsA> ra;
   AtRing<kAtSlotsB> rb;
   uint32_t hph = 0;
-  for (int64_t r = 0, u; (u = at_turn(r)) < nu; ++r) {
-    const AtQUnit x = at_q_unit(a, u);
-    if (x.n == 0) continue;
-    if (!mbar_wait<false>(&sh.held_empty, hph ^ 1u, wc)) return;
-    hph ^= 1u;
-    mbar_arrive_expect_tx(&sh.held_full, 2 * bytes);
-    const int32_t row = static_cast<int32_t>(x.q.q0) + x.t0;
+  AtWalk<AtQUnit> walk(a, nu);
+  AtStep f;
+  auto held = [&](int w, const CUtensorMap* m) {
+    if (!mbar_wait<false>(&sh.held_empty[w], hph ^ 1u, wc)) return false;
+    mbar_arrive_expect_tx(&sh.held_full[w], bytes);
 #pragma unroll
-    for (int b = 0; b < D / 64; ++b) {
-      tma_load_3d(smem + b * kAUnitBytes, mq, &sh.held_full, b * 64, x.h * a.G, row);
-      tma_load_3d(smem + T::tile_bytes + b * kAUnitBytes, mdo, &sh.held_full, b * 64, x.h * a.G, row);
+    for (int b = 0; b < D / 64; ++b)
+      tma_load_3d(smem + w * T::tile_bytes + b * kAUnitBytes, m, &sh.held_full[w], b * 64, walk.x.h * a.G,
+                  static_cast<int32_t>(walk.x.q.q0) + walk.x.t0);
+    return true;
+  };
+  while (walk.step(f)) {
+    const AtQUnit& x = walk.x;
+    const int32_t key = static_cast<int32_t>(x.q.k0) + (walk.i - 1) * kAtTile;
+    if (f.first && !held(0, mq)) return;
+    if (!mbar_wait<false>(&sh.a_empty[ra.slot], ra.phase ^ 1u, wc)) return;
+    mbar_arrive_expect_tx(&sh.a_full[ra.slot], T::tile_bytes);
+#pragma unroll
+    for (int b = 0; b < D / 64; ++b)
+      tma_load_3d(smem + T::ring_a + ra.slot * T::tile_bytes + b * kAUnitBytes, mk, &sh.a_full[ra.slot], b * 64, x.h, key);
+    ra.next();
+    if (f.ragged) mbar_arrive(&sh.z_ask[0]);
+    if (f.first) {
+      if (!held(1, mdo)) return;
+      hph ^= 1u;
     }
-    auto key_tile = [&](int32_t j) {
-      if (!mbar_wait<false>(&sh.a_empty[ra.slot], ra.phase ^ 1u, wc)) return false;
-      mbar_arrive_expect_tx(&sh.a_full[ra.slot], T::tile_bytes);
+    if (!mbar_wait<false>(&sh.b_empty[rb.slot], rb.phase ^ 1u, wc)) return;
+    mbar_arrive_expect_tx(&sh.b_full[rb.slot], T::tile_bytes);
 #pragma unroll
-      for (int b = 0; b < D / 64; ++b)
-        tma_load_3d(smem + T::ring_a + ra.slot * T::tile_bytes + b * kAUnitBytes, mk, &sh.a_full[ra.slot], b * 64, x.h,
-                    static_cast<int32_t>(x.q.k0) + j * kAtTile);
-      ra.next();
-      if (j + 1 == x.n && x.ragged) mbar_arrive(&sh.z_ask[0]);
-      return true;
-    };
-    if (!key_tile(0)) return;
-    for (int32_t j = 0; j < x.n; ++j) {  // in the order of use: V_j behind K_j, before K_{j+1}
-      if (!mbar_wait<false>(&sh.b_empty[rb.slot], rb.phase ^ 1u, wc)) return;
-      mbar_arrive_expect_tx(&sh.b_full[rb.slot], T::tile_bytes);
-#pragma unroll
-      for (int b = 0; b < D / 64; ++b)
-        tma_load_3d(smem + T::ring_b + rb.slot * T::tile_bytes + b * kAUnitBytes, mv, &sh.b_full[rb.slot], b * 64, x.h,
-                    static_cast<int32_t>(x.q.k0) + j * kAtTile);
-      rb.next();
-      if (j + 1 < x.n && !key_tile(j + 1)) return;
-    }
+    for (int b = 0; b < D / 64; ++b)
+      tma_load_3d(smem + T::ring_b + rb.slot * T::tile_bytes + b * kAUnitBytes, mv, &sh.b_full[rb.slot], b * 64, x.h, key);
+    rb.next();
   }
 }
 
@@ -646,58 +699,61 @@ __device__ __forceinline__ void at_dq_mma(AtBwdShared& sh, const AttnBwdArgs& a,
   AtRing<kAtSlotsA> ra, ra2;
   AtRing<kAtSlotsB> rb;
   AtRing<2> sb;                // score buffer of the next S
-  uint32_t hph = 0, ph = 0, cur = 0, zph = 0;
+  uint32_t hph[2] = {0, 0}, zph = 0, ph = 0, cur = 0;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     const bool ok = mbar_wait<false>(bar, parity, wc);
     tc_fence_after();
     return ok;
   };
-  for (int64_t r = 0, u; (u = at_turn(r)) < nu; ++r) {
-    const AtQUnit x = at_q_unit(a, u);
-    if (x.n == 0) continue;
-    auto scores = [&](int32_t j) {
-      if (!wait(&sh.a_full[ra.slot], ra.phase)) return false;
-      if (j + 1 == x.n && x.ragged && !wait(&sh.z_full[0], zph)) return false;
-      at_mma_ss<D>(tmem + sb.slot * 128, dq, dk_k + ra.slot * ts);
-      umma_commit(&sh.s_full[sb.slot]);
-      ra.next();
-      sb.next();
-      return true;
-    };
-    auto dprobs = [&](int32_t j) {
-      if (!wait(&sh.b_full[rb.slot], rb.phase)) return false;
-      at_mma_ss<D>(t_dp, ddo, dv_k + rb.slot * ts);
-      umma_commit(&sh.dp_full);
-      umma_commit(&sh.b_empty[rb.slot]);
-      rb.next();
-      return true;
-    };
-    if (!wait(&sh.held_full, hph)) break;
-    hph ^= 1u;
-    if (!scores(0) || !dprobs(0)) break;
-    if (x.n > 1 && !scores(1)) break;
-    if (x.n == 1) umma_commit(&sh.held_empty);
-    bool ok = true;
-    for (int32_t j = 0; j < x.n && ok; ++j) {
-      // One barrier for the whole tile: dP_{j+1} lets the next dS come, so nothing of this one may
-      // still be waited for behind it.
-      if (!wait(&sh.ds_full[0], ph)) { ok = false; break; }
-      if (j + 1 < x.n) {
-        if (!dprobs(j + 1)) { ok = false; break; }
-        if (j + 2 == x.n) umma_commit(&sh.held_empty);
-      }
-#pragma unroll
-      for (int half = 0; half < 2; ++half)
-        at_mma_ts<D>(t_dq, tmem + cur * 128, dk_mn + ra2.slot * ts, half, j == 0);
-      umma_commit(&sh.a_empty[ra2.slot]);
-      if (j + 1 == x.n) umma_commit(&sh.acc_full);
-      ra2.next();
-      cur ^= 1u;
-      ph ^= 1u;
-      if (j + 2 < x.n && !scores(j + 2)) ok = false;
+  auto held = [&](int w, const AtStep& f) {
+    if (!f.first) return true;
+    hph[w] ^= 1u;
+    return wait(&sh.held_full[w], hph[w] ^ 1u);
+  };
+  auto scores = [&](const AtStep& f) {
+    if (!wait(&sh.a_full[ra.slot], ra.phase) || !held(0, f)) return false;
+    if (f.ragged) {
+      if (!wait(&sh.z_full[0], zph)) return false;
+      zph ^= 1u;
     }
-    if (!ok) break;
-    if (x.ragged) zph ^= 1u;
+    at_mma_ss<D>(tmem + sb.slot * 128, dq, dk_k + ra.slot * ts);
+    umma_commit(&sh.s_full[sb.slot]);
+    if (f.last) umma_commit(&sh.held_empty[0]);
+    ra.next();
+    sb.next();
+    return true;
+  };
+  auto dprobs = [&](const AtStep& f) {
+    if (!wait(&sh.b_full[rb.slot], rb.phase) || !held(1, f)) return false;
+    at_mma_ss<D>(t_dp, ddo, dv_k + rb.slot * ts);
+    umma_commit(&sh.dp_full);
+    umma_commit(&sh.b_empty[rb.slot]);
+    if (f.last) umma_commit(&sh.held_empty[1]);
+    rb.next();
+    return true;
+  };
+  AtWalk<AtQUnit> walk(a, nu);
+  AtStep f, f1, f2;
+  bool go = walk.step(f) && scores(f) && dprobs(f);
+  bool n1 = go && walk.step(f1);
+  if (n1) go = scores(f1);
+  while (go) {
+    const bool n2 = n1 && walk.step(f2);
+    // One barrier for the whole tile: the next dP lets the next dS come, so nothing of this one may
+    // still be waited for behind it.
+    if (!wait(&sh.ds_full[0], ph) || (n1 && !dprobs(f1))) break;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) at_mma_ts<D>(t_dq, tmem + cur * 128, dk_mn + ra2.slot * ts, half, f.first);
+    umma_commit(&sh.a_empty[ra2.slot]);
+    if (f.last) umma_commit(&sh.acc_full);
+    ra2.next();
+    cur ^= 1u;
+    ph ^= 1u;
+    if (n2 && !scores(f2)) break;
+    go = n1;
+    f = f1;
+    f1 = f2;
+    n1 = n2;
   }
   umma_commit(&sh.done);
   mbar_wait<false>(&sh.done, 0u, wc);
@@ -711,7 +767,8 @@ __device__ __forceinline__ void at_dq_ragged(AtBwdShared& sh, const AttnBwdArgs&
   AtRing<kAtSlotsA> ra;
   uint32_t ph = 0;
   for (int64_t r = 0, u; (u = at_turn(r)) < nu; ++r) {
-    const AtQUnit x = at_q_unit(a, u);
+    AtQUnit x;
+    x.fetch(a, u);
     if (x.n == 0) continue;
     ra.skip(x.n - 1);
     if (x.ragged) {
@@ -736,11 +793,25 @@ __device__ __forceinline__ void at_dq_probs(AtBwdShared& sh, const AttnBwdArgs& 
   AtRing<2> sb;
   const float2 cc = make_float2(a.c, a.c);
   auto wait = [&](uint64_t* bar, uint32_t parity) { return at_wait(bar, parity, wc); };
+  // A unit's sum is stored when the next unit's first p is computed: its scores are there by then.
+  uint16_t* done_o = nullptr;
+  bool done_valid = false, pending = false;
+  auto store = [&]() {
+    if (!wait(&sh.acc_full, aph)) return false;
+    aph ^= 1u;
+#pragma unroll
+    for (int b = 0; b < D / 64; ++b)
+      at_store16(tmem + lanes + 384 + X * (D / 4) + b * 16, a.scale, done_o + b * 16, done_valid);
+    pending = false;
+    return true;
+  };
   for (int64_t r = 0, u; (u = at_turn(r)) < nu; ++r) {
-    const AtQUnit x = at_q_unit(a, u);
+    AtQUnit x;
+    x.fetch(a, u);
     const int32_t tok = x.t0 + tok_in;
     const bool valid = tok_in < a.tpt && tok < x.q.lq;
-    const int32_t vis = valid ? attn_visible(tok, x.q.lq, x.q.lk, a.causal) : 0;
+    // rows without a query see all, so that they do not make their warp mask every tile
+    const int32_t vis = valid ? attn_visible(tok, x.q.lq, x.q.lk, a.causal) : 0x7fffffff;
     uint16_t* o = a.o0 + (x.q.q0 + tok) * a.ld0 + static_cast<int64_t>(x.h * a.G + g) * D + X * (D / 4);
     if (x.n == 0) {  // no key to see
       if (valid)
@@ -770,6 +841,7 @@ __device__ __forceinline__ void at_dq_probs(AtBwdShared& sh, const AttnBwdArgs& 
           p[half][e] = at_ex2(e, fma2(at_pair(s[half], e), cc, nl));
         }
       }
+      if (pending && !store()) return;
       if (!wait(&sh.dp_full, ph)) return;
       at_get(t_dp, s);
 #pragma unroll
@@ -790,12 +862,11 @@ __device__ __forceinline__ void at_dq_probs(AtBwdShared& sh, const AttnBwdArgs& 
       sb.next();
       ph ^= 1u;
     }
-    if (!wait(&sh.acc_full, aph)) return;
-    aph ^= 1u;
-#pragma unroll
-    for (int b = 0; b < D / 64; ++b)
-      at_store16(tmem + lanes + 384 + X * (D / 4) + b * 16, a.scale, o + b * 16, valid);
+    pending = true;
+    done_o = o;
+    done_valid = valid;
   }
+  if (pending) store();
 }
 
 template <int D>
