@@ -243,7 +243,12 @@ struct AttnFwdArgs {
   uint64_t limit_ns;
 };
 
-constexpr int kAtFwdThreads = 320;  // warps 0-3 and 4-7: softmax of the two row tiles; 8: TMA; 9: MMA
+// Warps 0-3 and 4-7: softmax of the two row tiles, a row to a thread; 8: TMA; 9: MMA; 10: ragged value tiles.
+// A row's 128 scores stay in registers: the last four warps give up some of theirs
+// (2 x 208 + 88 = 3 x 168, what the block is launched with).
+constexpr int kAtFwdThreads = 384;
+constexpr int kAtFwdSoft = 8;
+constexpr int kAtSoftRegs = 208, kAtOtherRegs = 88;
 
 template <int D>
 struct AtFwdTile {
@@ -253,8 +258,9 @@ struct AtFwdTile {
 };
 struct AtFwdShared {
   uint64_t full[8], empty[8];
-  uint64_t q_full, q_empty;
-  uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t z_ask[8], z_full[8];     // a ragged value tile: loading; has its zeros
+  uint64_t q_full[2], q_empty[2];
+  uint64_t s_full[2], p_full[2][2], o_full[2];  // of the row tiles; P in halves of the keys
   uint64_t done;
   uint32_t tmem_base;
   volatile uint32_t abort_flag;
@@ -316,25 +322,54 @@ struct AtUnit {
   int32_t jb;       // first key tile
   int32_t je[2];    // end of each row tile's key tiles
   int32_t n;        // end of the unit's
-};
-__device__ __forceinline__ AtUnit at_unit(const AttnFwdArgs& a, int64_t u) {
-  AtUnit x;
-  const AttnUnit w = a.units[u / a.Hkv];
-  x.h = static_cast<int32_t>(u % a.Hkv);
-  x.q = a.seqs[w.seq];
-  x.t0 = w.t0;
-  x.jb = w.c0 * kAtChunkTiles;
+  __device__ __forceinline__ int32_t tiles() const { return n > jb ? n - jb : 0; }
+  __device__ __forceinline__ bool ragged(int32_t j) const { return q.lk - j * kAtTile < kAtTile; }
+  __device__ __forceinline__ void fetch(const AttnFwdArgs& a, int64_t u) {
+    const AttnUnit w = a.units[u / a.Hkv];
+    h = static_cast<int32_t>(u % a.Hkv);
+    q = a.seqs[w.seq];
+    t0 = w.t0;
+    jb = w.c0 * kAtChunkTiles;
 #pragma unroll
-  for (int X = 0; X < 2; ++X) {
-    const int32_t first = w.t0 + X * a.tpt;
-    int32_t last = first + a.tpt;
-    last = (last < x.q.lq ? last : x.q.lq) - 1;
-    const int32_t n = last < first ? 0 : (attn_visible(last, x.q.lq, x.q.lk, a.causal) + kAtTile - 1) / kAtTile;
-    x.je[X] = n < w.c1 * kAtChunkTiles ? n : w.c1 * kAtChunkTiles;
+    for (int X = 0; X < 2; ++X) {
+      const int32_t first = w.t0 + X * a.tpt;
+      int32_t last = first + a.tpt;
+      last = (last < q.lq ? last : q.lq) - 1;
+      const int32_t m = last < first ? 0 : (attn_visible(last, q.lq, q.lk, a.causal) + kAtTile - 1) / kAtTile;
+      je[X] = m < w.c1 * kAtChunkTiles ? m : w.c1 * kAtChunkTiles;
+    }
+    n = je[0] > je[1] ? je[0] : je[1];
   }
-  x.n = x.je[0] > x.je[1] ? x.je[0] : x.je[1];
-  return x;
-}
+};
+
+// The tiles of a CTA's units one behind another.  The next unit's description is fetched a unit ahead,
+// so that nothing waits for it at the turn.
+template <class Args, class Unit>
+struct AtWalk {
+  const Args& a;
+  const int64_t nu;
+  int64_t r = 0;
+  Unit x, nx;            // the current unit and the next one
+  int32_t i = 0, n = 0;  // its tiles taken, and all of them
+  bool more;
+  __device__ __forceinline__ AtWalk(const Args& args, int64_t units) : a(args), nu(units) {
+    more = at_turn(0) < nu;
+    if (more) nx.fetch(a, at_turn(0));
+  }
+  __device__ __forceinline__ bool step() {
+    while (i == n) {
+      if (!more) return false;
+      x = nx;
+      i = 0;
+      n = x.tiles();
+      const int64_t u = at_turn(++r);
+      more = u < nu;
+      if (more) nx.fetch(a, u);
+    }
+    ++i;
+    return true;
+  }
+};
 
 template <int D>
 __device__ __forceinline__ void at_fwd_load(AtFwdShared& sh, const AttnFwdArgs& a, uint32_t smem, int64_t nu,
@@ -346,30 +381,34 @@ __device__ __forceinline__ void at_fwd_load(AtFwdShared& sh, const AttnFwdArgs& 
   tma_prefetch_desc(mv);
   const uint32_t ring = smem + 2 * T::tile_bytes;
   const uint32_t qbytes = static_cast<uint32_t>(a.tpt * a.G) * 128u * (D / 64);
-  uint32_t slot = 0, phase = 0, qph = 0;
-  for (int64_t r = 0, u; (u = at_turn(r)) < nu; ++r) {
-    const AtUnit x = at_unit(a, u);
-    if (x.n <= x.jb) continue;
-    if (!mbar_wait<false>(&sh.q_empty, qph ^ 1u, wc)) return;
-    qph ^= 1u;
-    const int nx = x.je[1] > x.jb ? 2 : 1;
-    mbar_arrive_expect_tx(&sh.q_full, qbytes * nx);
-    for (int X = 0; X < nx; ++X)
+  uint32_t slot = 0, phase = 0, qph[2] = {0, 0};
+  AtWalk<AttnFwdArgs, AtUnit> walk(a, nu);
+  while (walk.step()) {
+    const AtUnit& x = walk.x;
+    const int32_t j = x.jb + walk.i - 1;
+    if (walk.i == 1) {
 #pragma unroll
-      for (int b = 0; b < D / 64; ++b)
-        tma_load_3d(smem + X * T::tile_bytes + b * kAUnitBytes, mq, &sh.q_full, b * 64, x.h * a.G,
-                    static_cast<int32_t>(x.q.q0) + x.t0 + X * a.tpt);
-    for (int32_t j = x.jb; j < x.n; ++j) {
-#pragma unroll
-      for (int kv = 0; kv < 2; ++kv) {
-        if (!mbar_wait<false>(&sh.empty[slot], phase ^ 1u, wc)) return;
-        mbar_arrive_expect_tx(&sh.full[slot], T::tile_bytes);
+      for (int X = 0; X < 2; ++X) {
+        if (x.je[X] <= x.jb) continue;
+        if (!mbar_wait<false>(&sh.q_empty[X], qph[X] ^ 1u, wc)) return;
+        qph[X] ^= 1u;
+        mbar_arrive_expect_tx(&sh.q_full[X], qbytes);
 #pragma unroll
         for (int b = 0; b < D / 64; ++b)
-          tma_load_3d(ring + slot * T::tile_bytes + b * kAUnitBytes, kv ? mv : mk, &sh.full[slot], b * 64, x.h,
-                      static_cast<int32_t>(x.q.k0) + j * kAtTile);
-        ring_advance(slot, phase, T::slots);
+          tma_load_3d(smem + X * T::tile_bytes + b * kAUnitBytes, mq, &sh.q_full[X], b * 64, x.h * a.G,
+                      static_cast<int32_t>(x.q.q0) + x.t0 + X * a.tpt);
       }
+    }
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) {
+      if (!mbar_wait<false>(&sh.empty[slot], phase ^ 1u, wc)) return;
+      mbar_arrive_expect_tx(&sh.full[slot], T::tile_bytes);
+#pragma unroll
+      for (int b = 0; b < D / 64; ++b)
+        tma_load_3d(ring + slot * T::tile_bytes + b * kAUnitBytes, kv ? mv : mk, &sh.full[slot], b * 64, x.h,
+                    static_cast<int32_t>(x.q.k0) + j * kAtTile);
+      if (kv && x.ragged(j)) mbar_arrive(&sh.z_ask[slot]);
+      ring_advance(slot, phase, T::slots);
     }
   }
 }
@@ -387,96 +426,136 @@ __device__ __forceinline__ void at_zero_rows(uint8_t* tile, int valid) {
   __syncwarp();
 }
 
+// Value rows behind a sequence's last key, before the products see them.  The loading thread asks with the
+// tile's load; until the tile is used up its slot, and with it the pair of barriers, belongs to it.
 template <int D>
-__device__ __forceinline__ void at_fwd_mma(AtFwdShared& sh, const AttnFwdArgs& a, uint8_t* smem_p, int64_t nu,
+__device__ __forceinline__ void at_fwd_ragged(AtFwdShared& sh, const AttnFwdArgs& a, uint8_t* smem_p, int64_t nu) {
+  using T = AtFwdTile<D>;
+  const WaitCtl wc{&sh.abort_flag, a.status, a.limit_ns};
+  uint32_t at = 0, used = 0;  // ring position of the unit's first tile, a phase for each slot
+  for (int64_t r = 0, u; (u = at_turn(r)) < nu; ++r) {
+    AtUnit x;
+    x.fetch(a, u);
+    const uint32_t tiles = static_cast<uint32_t>(x.tiles());
+    if (tiles == 0) continue;
+    const uint32_t pos = at + 2 * tiles - 1;  // of the last value tile, modulo two rounds of the ring
+    const uint32_t slot = pos % T::slots, phase = pos / T::slots & 1u;
+    if (x.ragged(x.n - 1)) {
+      if (!at_wait(&sh.z_ask[slot], (used >> slot) & 1u, wc) || !at_wait(&sh.full[slot], phase, wc)) return;
+      used ^= 1u << slot;
+      at_zero_rows<D>(smem_p + (2 + slot) * T::tile_bytes, x.q.lk - (x.n - 1) * kAtTile);
+      if ((threadIdx.x & 31) == 0) mbar_arrive(&sh.z_full[slot]);
+    }
+    at = (at + 2 * tiles) % (2 * T::slots);
+  }
+}
+
+// One thread.  A row tile's next scores go behind its product with the values, into the columns that held
+// its P; the other row tile's softmax runs meanwhile.
+struct AtFwdStep {
+  bool on[2];        // the row tile sees this key tile
+  bool begin;        // first tile of the unit
+  bool q_last[2];    // last one for the row tile
+  bool fresh;        // first of a chunk
+  bool o_end[2];     // O is complete behind it
+  bool ragged;
+};
+template <int D>
+__device__ __forceinline__ void at_fwd_mma(AtFwdShared& sh, const AttnFwdArgs& a, uint32_t smem, int64_t nu,
                                            uint32_t tmem) {
   using T = AtFwdTile<D>;
   const WaitCtl wc{&sh.abort_flag, a.status, a.limit_ns};
-  const uint32_t smem = smem_u32(smem_p);
   constexpr uint32_t idesc_s = idesc_bf16(128, 128, false, false);
   constexpr uint32_t idesc_o = idesc_bf16(128, D, false, true);
   constexpr uint64_t blk = kAUnitBytes >> 4;
   const uint64_t dq0 = sdesc_k_sw128(smem);
   const uint64_t dk0 = sdesc_k_sw128(smem + 2 * T::tile_bytes);
   const uint64_t dv0 = sdesc_mn_sw128(smem + 2 * T::tile_bytes, kAUnitBytes);
-  uint32_t slot = 0, phase = 0, qph = 0, pph[2] = {0, 0};
-  auto scores = [&](int X, uint32_t ks) {  // S_X = Q_X K^T
-    if (elect_one()) {
-      const uint64_t da = dq0 + X * (T::tile_bytes >> 4), db = dk0 + ks * (T::tile_bytes >> 4);
-#pragma unroll
-      for (int b = 0; b < D / 64; ++b)
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          umma_bf16(tmem + X * 128, da + b * blk + 2 * k, db + b * blk + 2 * k, idesc_s, (b | k) ? 1u : 0u);
-      umma_commit(&sh.s_full[X]);
-    }
-  };
-  auto values = [&](int X, uint32_t vs, bool first) {  // O_X += P_X V
-    if (elect_one()) {
-      const uint64_t db = dv0 + vs * (T::tile_bytes >> 4);
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        umma_bf16_ta(tmem + 256 + X * D, tmem + X * 128 + k * 8, db + k * (2048 >> 4), idesc_o,
-                     (k > 0 || !first) ? 1u : 0u);
-    }
-  };
-  for (int64_t r = 0, u; (u = at_turn(r)) < nu; ++r) {
-    const AtUnit x = at_unit(a, u);
-    if (x.n <= x.jb) continue;
-    if (!__all_sync(0xffffffffu, mbar_wait<false>(&sh.q_full, qph, wc))) break;
-    qph ^= 1u;
-    if (!__all_sync(0xffffffffu, mbar_wait<false>(&sh.full[slot], phase, wc))) break;
+  uint32_t slot = 0, phase = 0, qph[2] = {0, 0}, pph[2] = {0, 0}, zph = 0;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    const bool ok = mbar_wait<false>(bar, parity, wc);
     tc_fence_after();
-    for (int X = 0; X < 2; ++X)
-      if (x.jb < x.je[X]) scores(X, slot);
-    if (elect_one()) {
-      umma_commit(&sh.empty[slot]);
-      if (x.jb + 1 == x.n) umma_commit(&sh.q_empty);
-    }
-    ring_advance(slot, phase, T::slots);
-    bool ok = true;
-    for (int32_t j = x.jb; j < x.n; ++j) {
-      const uint32_t vs = slot, vph = phase;
-      ring_advance(slot, phase, T::slots);
-      if (!__all_sync(0xffffffffu, mbar_wait<false>(&sh.full[vs], vph, wc))) { ok = false; break; }
-      const int32_t rows = x.q.lk - j * kAtTile;
-      if (rows < kAtTile) at_zero_rows<D>(smem_p + (2 + vs) * T::tile_bytes, rows);
-      const bool next = j + 1 < x.n;
-      const bool first = j % kAtChunkTiles == 0;
-      const bool last = (j + 1) % kAtChunkTiles == 0;
-      bool have_k = false;
+    return ok;
+  };
+  AtWalk<AttnFwdArgs, AtUnit> walk(a, nu);
+  auto step = [&](AtFwdStep& f) {
+    if (!walk.step()) return false;
+    const AtUnit& x = walk.x;
+    const int32_t j = x.jb + walk.i - 1;
+    f.begin = walk.i == 1;
+    f.fresh = j % kAtChunkTiles == 0;
+    f.ragged = x.ragged(j);
 #pragma unroll
-      for (int X = 0; X < 2; ++X) {
-        if (j < x.je[X]) {
-          if (!__all_sync(0xffffffffu, mbar_wait<false>(&sh.p_full[X], pph[X], wc))) { ok = false; break; }
-          pph[X] ^= 1u;
-          tc_fence_after();
-          values(X, vs, first);
-          if (elect_one() && (last || j + 1 == x.je[X])) umma_commit(&sh.o_full[X]);
-        }
-        if (next && !have_k) {
-          if (!__all_sync(0xffffffffu, mbar_wait<false>(&sh.full[slot], phase, wc))) { ok = false; break; }
-          tc_fence_after();
-          have_k = true;
-        }
-        if (j + 1 < x.je[X]) scores(X, slot);
-      }
-      if (!ok) break;
-      if (elect_one()) {
-        umma_commit(&sh.empty[vs]);
-        if (next) umma_commit(&sh.empty[slot]);
-        if (j + 2 == x.n) umma_commit(&sh.q_empty);
-      }
-      if (next) ring_advance(slot, phase, T::slots);
+    for (int X = 0; X < 2; ++X) {
+      f.on[X] = j < x.je[X];
+      f.q_last[X] = j + 1 == x.je[X];
+      f.o_end[X] = f.q_last[X] || (j + 1) % kAtChunkTiles == 0;
     }
-    if (!ok) break;
+    return true;
+  };
+  auto scores = [&](const AtFwdStep& f, int X, uint32_t ks) {  // S_X = Q_X K^T
+    if (f.begin) {
+      if (!wait(&sh.q_full[X], qph[X])) return false;
+      qph[X] ^= 1u;
+    }
+    const uint64_t da = dq0 + X * (T::tile_bytes >> 4), db = dk0 + ks * (T::tile_bytes >> 4);
+#pragma unroll
+    for (int b = 0; b < D / 64; ++b)
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        umma_bf16(tmem + X * 128, da + b * blk + 2 * k, db + b * blk + 2 * k, idesc_s, (b | k) ? 1u : 0u);
+    umma_commit(&sh.s_full[X]);
+    if (f.q_last[X]) umma_commit(&sh.q_empty[X]);
+    return true;
+  };
+  AtFwdStep f, fn;
+  bool go = step(f) && wait(&sh.full[slot], phase);
+  if (go) {
+#pragma unroll
+    for (int X = 0; X < 2; ++X)
+      if (go && f.on[X]) go = scores(f, X, slot);
+    umma_commit(&sh.empty[slot]);
+    ring_advance(slot, phase, T::slots);
   }
-  __syncwarp();
-  if (elect_one()) umma_commit(&sh.done);
+  while (go) {
+    const bool next = step(fn);
+    const uint32_t vs = slot;
+    go = wait(&sh.full[vs], phase);
+    ring_advance(slot, phase, T::slots);
+    if (go && f.ragged) {
+      go = wait(&sh.z_full[vs], (zph >> vs) & 1u);
+      zph ^= 1u << vs;
+    }
+    const uint64_t db = dv0 + vs * (T::tile_bytes >> 4);
+#pragma unroll
+    for (int X = 0; X < 2; ++X) {
+      if (go && f.on[X]) {  // O_X += P_X V
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          go = go && wait(&sh.p_full[X][half], pph[X]);
+          if (go)
+#pragma unroll
+            for (int k = 4 * half; k < 4 * half + 4; ++k)
+              umma_bf16_ta(tmem + 256 + X * D, tmem + X * 128 + k * 8, db + k * (2048 >> 4), idesc_o,
+                           (k > 0 || !f.fresh) ? 1u : 0u);
+        }
+        pph[X] ^= 1u;
+        if (f.o_end[X]) umma_commit(&sh.o_full[X]);
+      }
+      if (X == 0 && next) go = go && wait(&sh.full[slot], phase);
+      if (next && go && fn.on[X]) go = scores(fn, X, slot);
+    }
+    umma_commit(&sh.empty[vs]);
+    if (!next) break;
+    umma_commit(&sh.empty[slot]);
+    ring_advance(slot, phase, T::slots);
+    f = fn;
+  }
+  umma_commit(&sh.done);
   mbar_wait<false>(&sh.done, 0u, wc);
 }
 
-// Softmax and output of row tile X (128 threads, one row each).
+// Softmax and output of row tile X (128 threads, a row each).
 template <int D>
 __device__ __forceinline__ void at_fwd_softmax(AtFwdShared& sh, const AttnFwdArgs& a, int X, int64_t nu, bool split,
                                                uint32_t tmem) {
@@ -488,8 +567,10 @@ __device__ __forceinline__ void at_fwd_softmax(AtFwdShared& sh, const AttnFwdArg
   const int tok_in = row / a.G, g = row - tok_in * a.G;
   float4* scr = reinterpret_cast<float4*>(a.scratch) + ((static_cast<int64_t>(blockIdx.x) * 2 + X) * (D / 4)) * 128 + row;
   uint32_t sph = 0, oph = 0;
+  const float2 cc = make_float2(a.c, a.c);
   for (int64_t r = 0, u; (u = at_turn(r)) < nu; ++r) {
-    const AtUnit x = at_unit(a, u);
+    AtUnit x;
+    x.fetch(a, u);
     const int32_t tok = x.t0 + X * a.tpt + tok_in;
     const bool valid = tok_in < a.tpt && tok < x.q.lq;
     const bool warp_valid = __any_sync(0xffffffffu, valid);
@@ -510,9 +591,8 @@ __device__ __forceinline__ void at_fwd_softmax(AtFwdShared& sh, const AttnFwdArg
     float m = -INFINITY, l = 0.f;          // of the chunk
     float m_run = -INFINITY, l_run = 0.f;  // of the chunks before
     for (int32_t j = x.jb; j < x.je[X]; ++j) {
-      if (!__all_sync(0xffffffffu, mbar_wait<false>(&sh.s_full[X], sph, wc))) return;
+      if (!at_wait(&sh.s_full[X], sph, wc)) return;
       sph ^= 1u;
-      tc_fence_after();
       const bool first = j % kAtChunkTiles == 0;
       if (first) m = -INFINITY, l = 0.f;
       if (warp_valid) {
@@ -536,7 +616,9 @@ __device__ __forceinline__ void at_fwd_softmax(AtFwdShared& sh, const AttnFwdArg
         for (int b = 0; b < 4; ++b) {
           mx[b] = __uint_as_float(s[b][0]);
 #pragma unroll
-          for (int e = 1; e < 32; ++e) mx[b] = fmaxf(mx[b], __uint_as_float(s[b][e]));
+          for (int e = 1; e < 31; e += 2)
+            mx[b] = fmaxf(fmaxf(mx[b], __uint_as_float(s[b][e])), __uint_as_float(s[b][e + 1]));
+          mx[b] = fmaxf(mx[b], __uint_as_float(s[b][31]));
         }
         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.c;
         if (first) {
@@ -544,48 +626,52 @@ __device__ __forceinline__ void at_fwd_softmax(AtFwdShared& sh, const AttnFwdArg
         } else {
           const bool raise = top > m + 8.f;
           if (__any_sync(0xffffffffu, raise)) {
+            at_rare();
             // S of this tile was issued behind the last product into O: O is complete
             const float alpha = raise ? attn_join_scale(m, top) : 1.f;
             if (raise) m = top;
             l *= alpha;
 #pragma unroll 1
-            for (int b = 0; b < D / 32; ++b) {
-              uint32_t o[32];
-              tmem_ld32(to + b * 32, o);
+            for (int b = 0; b < D / 16; ++b) {
+              uint32_t o[16];
+              tmem_ld16(to + b * 16, o);
               tmem_ld_wait();
-              tmem_ld_pin(o);
+              tmem_ld_pin16(o);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-              tmem_st32(to + b * 32, o);
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+              tmem_st16(to + b * 16, o);
             }
           }
         }
         const float mu = m == -INFINITY ? 0.f : -m;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        const float2 mm = make_float2(mu, mu);
+        float2 sum[2] = {make_float2(l, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-        for (int b = 0; b < 4; b += 2) {
+        for (int half = 0; half < 2; ++half) {
           uint32_t p[32];
 #pragma unroll
-          for (int e = 0; e < 64; e += 2) {
-            const float p0 = ex2_approx(fmaf(__uint_as_float(s[b + e / 32][e % 32]), a.c, mu));
-            const float p1 = ex2_approx(fmaf(__uint_as_float(s[b + e / 32][e % 32 + 1]), a.c, mu));
-            sum[(e / 2) % 2 * 2] += p0;
-            sum[(e / 2) % 2 * 2 + 1] += p1;
-            p[e / 2] = pack_bf16x2(p0, p1);  // bf16 terms: what the tensor cores take; l keeps fp32
+          for (int e = 0; e < 32; ++e) {
+            const uint32_t(&c)[32] = s[2 * half + e / 16];
+            const float2 v = make_float2(__uint_as_float(c[2 * (e % 16)]), __uint_as_float(c[2 * (e % 16) + 1]));
+            const float2 y = at_ex2(e, fma2(v, cc, mm));
+            sum[e % 2] = add2(sum[e % 2], y);
+            p[e] = pack_bf16x2(y.x, y.y);  // bf16 terms: what the tensor cores take; l keeps fp32
           }
-          tmem_st32(ts + b * 16, p);
+          tmem_st32(ts + half * 32, p);
+          tmem_st_wait();
+          tc_fence_before();
+          mbar_arrive(&sh.p_full[X][half]);
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        tmem_st_wait();
+        l = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+      } else {
+        mbar_arrive(&sh.p_full[X][0]);
+        mbar_arrive(&sh.p_full[X][1]);
       }
-      tc_fence_before();
-      mbar_arrive(&sh.p_full[X]);
       const bool last = j + 1 == x.je[X];
       if (!last && (j + 1) % kAtChunkTiles != 0) continue;
       // the chunk's end
-      if (!__all_sync(0xffffffffu, mbar_wait<false>(&sh.o_full[X], oph, wc))) return;
+      if (!at_wait(&sh.o_full[X], oph, wc)) return;
       oph ^= 1u;
-      tc_fence_after();
       if (!warp_valid) continue;
       const bool fresh = j - x.jb < kAtChunkTiles;  // no chunk before it in this unit
       if (joined) {
@@ -618,11 +704,11 @@ __device__ __forceinline__ void at_fwd_softmax(AtFwdShared& sh, const AttnFwdArg
         if (!fresh) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const float4 r = scr[(b * 8 + e) * 128];
-            o[4 * e] = __float_as_uint(fmaf(__uint_as_float(o[4 * e]), kb, r.x * ka));
-            o[4 * e + 1] = __float_as_uint(fmaf(__uint_as_float(o[4 * e + 1]), kb, r.y * ka));
-            o[4 * e + 2] = __float_as_uint(fmaf(__uint_as_float(o[4 * e + 2]), kb, r.z * ka));
-            o[4 * e + 3] = __float_as_uint(fmaf(__uint_as_float(o[4 * e + 3]), kb, r.w * ka));
+            const float4 q = scr[(b * 8 + e) * 128];
+            o[4 * e] = __float_as_uint(fmaf(__uint_as_float(o[4 * e]), kb, q.x * ka));
+            o[4 * e + 1] = __float_as_uint(fmaf(__uint_as_float(o[4 * e + 1]), kb, q.y * ka));
+            o[4 * e + 2] = __float_as_uint(fmaf(__uint_as_float(o[4 * e + 2]), kb, q.z * ka));
+            o[4 * e + 3] = __float_as_uint(fmaf(__uint_as_float(o[4 * e + 3]), kb, q.w * ka));
           }
         }
         if (!last) {
@@ -641,7 +727,8 @@ __device__ __forceinline__ void at_fwd_softmax(AtFwdShared& sh, const AttnFwdArg
                 make_uint4(p[4 * e], p[4 * e + 1], p[4 * e + 2], p[4 * e + 3]);
         }
       }
-      if (last && valid) *lse = m_run == -INFINITY ? -INFINITY : fmaf(m_run, 0.69314718055994531f, logf(l_run));
+      if (last && valid)
+        *lse = m_run == -INFINITY ? -INFINITY : fmaf(m_run, 0.69314718055994531f, logf(l_run));
     }
   }
 }
@@ -658,19 +745,22 @@ __global__ void __launch_bounds__(kAtFwdThreads, 1)
     for (int i = 0; i < 8; ++i) {
       mbar_init(&sh.full[i], 1);
       mbar_init(&sh.empty[i], 1);
+      mbar_init(&sh.z_ask[i], 1);
+      mbar_init(&sh.z_full[i], 1);
     }
-    mbar_init(&sh.q_full, 1);
-    mbar_init(&sh.q_empty, 1);
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.q_full[i], 1);
+      mbar_init(&sh.q_empty[i], 1);
       mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.p_full[i], 128);
+      mbar_init(&sh.p_full[i][0], 128);
+      mbar_init(&sh.p_full[i][1], 128);
       mbar_init(&sh.o_full[i], 1);
     }
     mbar_init(&sh.done, 1);
     sh.abort_flag = 0u;
     fence_mbar_init_cluster();
   }
-  if (warp == 9) {
+  if (warp == kAtFwdSoft + 1) {
     tmem_alloc(&sh.tmem_base, 512);
     tmem_relinquish();
   }
@@ -683,13 +773,20 @@ __global__ void __launch_bounds__(kAtFwdThreads, 1)
   if (misaligned && threadIdx.x == 0) raise_status(a.status, 4 /* BI_ERR_CUDA */);
   const int64_t nu = misaligned ? 0 : static_cast<int64_t>(a.head->nunits) * a.Hkv;
   const bool split = a.head->split != 0;
-  if (warp < 8) {
+  if (warp < kAtFwdSoft) {
+    regs_take<kAtSoftRegs>();
     at_fwd_softmax<D>(sh, a, warp >> 2, nu, split, tmem);
-  } else if (warp == 8) {
-    if (lane == 0) at_fwd_load<D>(sh, a, smem, nu, &mq, &mk, &mv);
-    __syncwarp();
   } else {
-    at_fwd_mma<D>(sh, a, dsmem, nu, tmem);
+    regs_give<kAtOtherRegs>();
+    if (warp == kAtFwdSoft) {
+      if (lane == 0) at_fwd_load<D>(sh, a, smem, nu, &mq, &mk, &mv);
+      __syncwarp();
+    } else if (warp == kAtFwdSoft + 1) {
+      if (elect_one()) at_fwd_mma<D>(sh, a, smem, nu, tmem);
+      __syncwarp();
+    } else if (warp == kAtFwdSoft + 2) {
+      at_fwd_ragged<D>(sh, a, dsmem, nu);
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -698,7 +795,7 @@ __global__ void __launch_bounds__(kAtFwdThreads, 1)
     while (globaltimer_ns() - t0 < 50000u) {
     }
   }
-  if (warp == 9) {
+  if (warp == kAtFwdSoft + 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }

@@ -132,37 +132,17 @@ struct AtRing {
   }
 };
 
-// The tiles of a CTA's units one behind another.  The next unit's description is fetched a unit ahead,
-// so that nothing waits for it at the turn.
 struct AtStep {
   bool first, last, ragged;  // first and last tile of its unit; that has rows to clear
 };
 template <class Unit>
-struct AtWalk {
-  const AttnBwdArgs& a;
-  const int64_t nu;
-  int64_t r = 0;
-  Unit x, nx;           // the current unit and the next one
-  int32_t i = 0, n = 0;  // of its tiles
-  bool more;
-  __device__ __forceinline__ AtWalk(const AttnBwdArgs& args, int64_t units) : a(args), nu(units) {
-    more = at_turn(0) < nu;
-    if (more) nx.fetch(a, at_turn(0));
-  }
+struct AtBwdWalk : AtWalk<AttnBwdArgs, Unit> {
+  using AtWalk<AttnBwdArgs, Unit>::AtWalk;
   __device__ __forceinline__ bool step(AtStep& s) {
-    while (i == n) {
-      if (!more) return false;
-      x = nx;
-      i = 0;
-      n = x.tiles();
-      const int64_t u = at_turn(++r);
-      more = u < nu;
-      if (more) nx.fetch(a, u);
-    }
-    s.first = i == 0;
-    ++i;
-    s.last = i == n;
-    s.ragged = s.last && x.ragged;
+    if (!AtWalk<AttnBwdArgs, Unit>::step()) return false;
+    s.first = this->i == 1;
+    s.last = this->i == this->n;
+    s.ragged = s.last && this->x.ragged;
     return true;
   }
 };
@@ -319,7 +299,7 @@ __device__ __forceinline__ void at_dkv_load(AtBwdShared& sh, const AttnBwdArgs& 
   AtRing<kAtSlotsB> rb;
   AtRing<2> rs;
   uint32_t hph = 0;
-  AtWalk<AtKvUnit> walk(a, nu);
+  AtBwdWalk<AtKvUnit> walk(a, nu);
   AtStep f;
   auto held = [&](int w, const CUtensorMap* m) {
     if (!mbar_wait<false>(&sh.held_empty[w], hph ^ 1u, wc)) return false;
@@ -410,7 +390,7 @@ __device__ __forceinline__ void at_dkv_mma(AtBwdShared& sh, const AttnBwdArgs& a
     rb.next();
     return true;
   };
-  AtWalk<AtKvUnit> walk(a, nu);
+  AtBwdWalk<AtKvUnit> walk(a, nu);
   AtStep f, fn;
   bool go = walk.step(f) && scores(f) && dprobs(f);
   while (go) {
@@ -651,7 +631,7 @@ __device__ __forceinline__ void at_dq_load(AtBwdShared& sh, const AttnBwdArgs& a
   AtRing<kAtSlotsA> ra;
   AtRing<kAtSlotsB> rb;
   uint32_t hph = 0;
-  AtWalk<AtQUnit> walk(a, nu);
+  AtBwdWalk<AtQUnit> walk(a, nu);
   AtStep f;
   auto held = [&](int w, const CUtensorMap* m) {
     if (!mbar_wait<false>(&sh.held_empty[w], hph ^ 1u, wc)) return false;
@@ -732,7 +712,7 @@ __device__ __forceinline__ void at_dq_mma(AtBwdShared& sh, const AttnBwdArgs& a,
     rb.next();
     return true;
   };
-  AtWalk<AtQUnit> walk(a, nu);
+  AtBwdWalk<AtQUnit> walk(a, nu);
   AtStep f, f1, f2;
   bool go = walk.step(f) && scores(f) && dprobs(f);
   bool n1 = go && walk.step(f1);
