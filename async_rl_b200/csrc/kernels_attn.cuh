@@ -253,12 +253,15 @@ constexpr int kAtSoftRegs = 208, kAtOtherRegs = 88;
 template <int D>
 struct AtFwdTile {
   static constexpr int tile_bytes = kAtTile * D * 2;       // Q, K and V tiles: D / 64 blocks of [128][64]
-  static constexpr int slots = D == 128 ? 5 : 8;           // ring of K and V tiles
+  static constexpr int slots = D == 128 ? 5 : 12;          // ring of K and V tiles
   static constexpr int smem = (2 + slots) * tile_bytes;
 };
+constexpr uint32_t kAtPairs = 8;    // more than a ring of tiles can hold
 struct AtFwdShared {
-  uint64_t full[8], empty[8];
-  uint64_t z_ask[8], z_full[8];     // a ragged value tile: loading; has its zeros
+  // Pair g of the tiles of a CTA: the values of its tile g - 1 and the keys of tile g, what the products
+  // between two rounds of softmax read.
+  uint64_t full[kAtPairs], empty[kAtPairs];
+  uint64_t z_ask[kAtPairs], z_full[kAtPairs];  // its value tile is ragged: loading; has its zeros
   uint64_t q_full[2], q_empty[2];
   uint64_t s_full[2], p_full[2][2], o_full[2];  // of the row tiles; P in halves of the keys
   uint64_t done;
@@ -381,7 +384,20 @@ __device__ __forceinline__ void at_fwd_load(AtFwdShared& sh, const AttnFwdArgs& 
   tma_prefetch_desc(mv);
   const uint32_t ring = smem + 2 * T::tile_bytes;
   const uint32_t qbytes = static_cast<uint32_t>(a.tpt * a.G) * 128u * (D / 64);
-  uint32_t slot = 0, phase = 0, qph[2] = {0, 0};
+  uint32_t qph[2] = {0, 0}, g = 0;
+  // tile `pos` of the ring (keys of tile g at 2 g, values at 2 g + 1), for pair `pair`
+  auto load = [&](uint32_t pos, uint32_t pair, const CUtensorMap* m, int32_t h, int32_t row) {
+    if (pos >= T::slots) {
+      const uint32_t before = (pos - T::slots + 1) / 2;  // the pair that used the slot last
+      if (!mbar_wait<false>(&sh.empty[before % kAtPairs], before / kAtPairs & 1u, wc)) return false;
+    }
+    uint64_t* bar = &sh.full[pair % kAtPairs];
+    mbar_arrive_expect_tx(bar, T::tile_bytes);
+#pragma unroll
+    for (int b = 0; b < D / 64; ++b)
+      tma_load_3d(ring + pos % T::slots * T::tile_bytes + b * kAUnitBytes, m, bar, b * 64, h, row);
+    return true;
+  };
   AtWalk<AttnFwdArgs, AtUnit> walk(a, nu);
   while (walk.step()) {
     const AtUnit& x = walk.x;
@@ -399,18 +415,13 @@ __device__ __forceinline__ void at_fwd_load(AtFwdShared& sh, const AttnFwdArgs& 
                       static_cast<int32_t>(x.q.q0) + x.t0 + X * a.tpt);
       }
     }
-#pragma unroll
-    for (int kv = 0; kv < 2; ++kv) {
-      if (!mbar_wait<false>(&sh.empty[slot], phase ^ 1u, wc)) return;
-      mbar_arrive_expect_tx(&sh.full[slot], T::tile_bytes);
-#pragma unroll
-      for (int b = 0; b < D / 64; ++b)
-        tma_load_3d(ring + slot * T::tile_bytes + b * kAUnitBytes, kv ? mv : mk, &sh.full[slot], b * 64, x.h,
-                    static_cast<int32_t>(x.q.k0) + j * kAtTile);
-      if (kv && x.ragged(j)) mbar_arrive(&sh.z_ask[slot]);
-      ring_advance(slot, phase, T::slots);
-    }
+    if (g == 0) mbar_arrive(&sh.full[0]);  // no values in the first pair
+    const int32_t row = static_cast<int32_t>(x.q.k0) + j * kAtTile;
+    if (!load(2 * g, g, mk, x.h, row) || !load(2 * g + 1, g + 1, mv, x.h, row)) return;
+    ++g;
+    if (x.ragged(j)) mbar_arrive(&sh.z_ask[g % kAtPairs]);
   }
+  if (g > 0) mbar_arrive(&sh.full[g % kAtPairs]);  // no keys in the last one
 }
 
 // Rows [valid, 128) of a tile in shared memory become zeros (the whole warp): what lies behind a
@@ -432,34 +443,25 @@ template <int D>
 __device__ __forceinline__ void at_fwd_ragged(AtFwdShared& sh, const AttnFwdArgs& a, uint8_t* smem_p, int64_t nu) {
   using T = AtFwdTile<D>;
   const WaitCtl wc{&sh.abort_flag, a.status, a.limit_ns};
-  uint32_t at = 0, used = 0;  // ring position of the unit's first tile, a phase for each slot
+  uint32_t g = 0, used = 0;  // the unit's first tile, a phase for each pair of barriers
   for (int64_t r = 0, u; (u = at_turn(r)) < nu; ++r) {
     AtUnit x;
     x.fetch(a, u);
     const uint32_t tiles = static_cast<uint32_t>(x.tiles());
     if (tiles == 0) continue;
-    const uint32_t pos = at + 2 * tiles - 1;  // of the last value tile, modulo two rounds of the ring
-    const uint32_t slot = pos % T::slots, phase = pos / T::slots & 1u;
-    if (x.ragged(x.n - 1)) {
-      if (!at_wait(&sh.z_ask[slot], (used >> slot) & 1u, wc) || !at_wait(&sh.full[slot], phase, wc)) return;
-      used ^= 1u << slot;
-      at_zero_rows<D>(smem_p + (2 + slot) * T::tile_bytes, x.q.lk - (x.n - 1) * kAtTile);
-      if ((threadIdx.x & 31) == 0) mbar_arrive(&sh.z_full[slot]);
-    }
-    at = (at + 2 * tiles) % (2 * T::slots);
+    g += tiles;
+    if (!x.ragged(x.n - 1)) continue;
+    const uint32_t b = g % kAtPairs;
+    if (!at_wait(&sh.z_ask[b], (used >> b) & 1u, wc) || !at_wait(&sh.full[b], g / kAtPairs & 1u, wc)) return;
+    used ^= 1u << b;
+    at_zero_rows<D>(smem_p + (2 + (2 * g - 1) % T::slots) * T::tile_bytes, x.q.lk - (x.n - 1) * kAtTile);
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&sh.z_full[b]);
   }
 }
 
 // One thread.  A row tile's next scores go behind its product with the values, into the columns that held
-// its P; the other row tile's softmax runs meanwhile.
-struct AtFwdStep {
-  bool on[2];        // the row tile sees this key tile
-  bool begin;        // first tile of the unit
-  bool q_last[2];    // last one for the row tile
-  bool fresh;        // first of a chunk
-  bool o_end[2];     // O is complete behind it
-  bool ragged;
-};
+// its P; the other row tile's softmax runs meanwhile.  The loop over a unit's tiles is kept short: what the
+// thread does besides issuing has to fit into the time of 32 MMAs, 2048 clocks.
 template <int D>
 __device__ __forceinline__ void at_fwd_mma(AtFwdShared& sh, const AttnFwdArgs& a, uint32_t smem, int64_t nu,
                                            uint32_t tmem) {
@@ -468,88 +470,103 @@ __device__ __forceinline__ void at_fwd_mma(AtFwdShared& sh, const AttnFwdArgs& a
   constexpr uint32_t idesc_s = idesc_bf16(128, 128, false, false);
   constexpr uint32_t idesc_o = idesc_bf16(128, D, false, true);
   constexpr uint64_t blk = kAUnitBytes >> 4;
+  constexpr uint32_t ts = T::tile_bytes >> 4;
   const uint64_t dq0 = sdesc_k_sw128(smem);
   const uint64_t dk0 = sdesc_k_sw128(smem + 2 * T::tile_bytes);
   const uint64_t dv0 = sdesc_mn_sw128(smem + 2 * T::tile_bytes, kAUnitBytes);
-  uint32_t slot = 0, phase = 0, qph[2] = {0, 0}, pph[2] = {0, 0}, zph = 0;
+  uint32_t g = 0, kat = 0, vat = 0;      // pair; its tiles' slots times the tile's size
+  uint32_t qph[2] = {0, 0}, pph[2] = {0, 0}, zph = 0;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     const bool ok = mbar_wait<false>(bar, parity, wc);
     tc_fence_after();
     return ok;
   };
-  AtWalk<AttnFwdArgs, AtUnit> walk(a, nu);
-  auto step = [&](AtFwdStep& f) {
-    if (!walk.step()) return false;
-    const AtUnit& x = walk.x;
-    const int32_t j = x.jb + walk.i - 1;
-    f.begin = walk.i == 1;
-    f.fresh = j % kAtChunkTiles == 0;
-    f.ragged = x.ragged(j);
-#pragma unroll
-    for (int X = 0; X < 2; ++X) {
-      f.on[X] = j < x.je[X];
-      f.q_last[X] = j + 1 == x.je[X];
-      f.o_end[X] = f.q_last[X] || (j + 1) % kAtChunkTiles == 0;
-    }
-    return true;
-  };
-  auto scores = [&](const AtFwdStep& f, int X, uint32_t ks) {  // S_X = Q_X K^T
-    if (f.begin) {
-      if (!wait(&sh.q_full[X], qph[X])) return false;
-      qph[X] ^= 1u;
-    }
-    const uint64_t da = dq0 + X * (T::tile_bytes >> 4), db = dk0 + ks * (T::tile_bytes >> 4);
+  auto scores = [&](int X) {  // S_X = Q_X K^T
+    const uint64_t da = dq0 + X * ts, db = dk0 + kat;
 #pragma unroll
     for (int b = 0; b < D / 64; ++b)
 #pragma unroll
       for (int k = 0; k < 4; ++k)
         umma_bf16(tmem + X * 128, da + b * blk + 2 * k, db + b * blk + 2 * k, idesc_s, (b | k) ? 1u : 0u);
     umma_commit(&sh.s_full[X]);
-    if (f.q_last[X]) umma_commit(&sh.q_empty[X]);
+  };
+  auto values = [&](int X, bool fresh) {  // O_X += P_X V
+    const uint64_t db = dv0 + vat;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      if (!wait(&sh.p_full[X][half], pph[X])) return false;
+#pragma unroll
+      for (int k = 4 * half; k < 4 * half + 4; ++k)
+        umma_bf16_ta(tmem + 256 + X * D, tmem + X * 128 + k * 8, db + k * (2048 >> 4), idesc_o, (k > 0 || !fresh) ? 1u : 0u);
+    }
+    pph[X] ^= 1u;
     return true;
   };
-  AtFwdStep f, fn;
-  bool go = step(f) && wait(&sh.full[slot], phase);
-  if (go) {
+  auto first = [&](const AtUnit& x) {  // a unit's first scores
 #pragma unroll
     for (int X = 0; X < 2; ++X)
-      if (go && f.on[X]) go = scores(f, X, slot);
-    umma_commit(&sh.empty[slot]);
-    ring_advance(slot, phase, T::slots);
-  }
-  while (go) {
-    const bool next = step(fn);
-    const uint32_t vs = slot;
-    go = wait(&sh.full[vs], phase);
-    ring_advance(slot, phase, T::slots);
-    if (go && f.ragged) {
-      go = wait(&sh.z_full[vs], (zph >> vs) & 1u);
-      zph ^= 1u << vs;
-    }
-    const uint64_t db = dv0 + vs * (T::tile_bytes >> 4);
-#pragma unroll
-    for (int X = 0; X < 2; ++X) {
-      if (go && f.on[X]) {  // O_X += P_X V
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          go = go && wait(&sh.p_full[X][half], pph[X]);
-          if (go)
-#pragma unroll
-            for (int k = 4 * half; k < 4 * half + 4; ++k)
-              umma_bf16_ta(tmem + 256 + X * D, tmem + X * 128 + k * 8, db + k * (2048 >> 4), idesc_o,
-                           (k > 0 || !f.fresh) ? 1u : 0u);
-        }
-        pph[X] ^= 1u;
-        if (f.o_end[X]) umma_commit(&sh.o_full[X]);
+      if (x.je[X] > x.jb) {
+        if (!wait(&sh.q_full[X], qph[X])) return false;
+        qph[X] ^= 1u;
+        scores(X);
+        if (x.je[X] == x.jb + 1) umma_commit(&sh.q_empty[X]);
       }
-      if (X == 0 && next) go = go && wait(&sh.full[slot], phase);
-      if (next && go && fn.on[X]) go = scores(fn, X, slot);
+    return true;
+  };
+  auto turn = [&]() {  // on to the next pair
+    umma_commit(&sh.empty[g % kAtPairs]);
+    ++g;
+    vat = kat + ts == T::slots * ts ? 0u : kat + ts;
+    kat = vat + ts == T::slots * ts ? 0u : vat + ts;
+  };
+  AtUnit x, nx;
+  int64_t r = 0;
+  auto fetch = [&]() {  // the next unit that has tiles
+    for (int64_t u; (u = at_turn(r)) < nu;) {
+      ++r;
+      nx.fetch(a, u);
+      if (nx.tiles() > 0) return true;
     }
-    umma_commit(&sh.empty[vs]);
-    if (!next) break;
-    umma_commit(&sh.empty[slot]);
-    ring_advance(slot, phase, T::slots);
-    f = fn;
+    return false;
+  };
+  bool next = fetch();
+  bool go = next && wait(&sh.full[0], 0u) && first(nx);
+  if (go) turn();
+  while (go && next) {
+    x = nx;
+    next = fetch();
+    const int32_t n = x.n - x.jb, e0 = x.je[0] - x.jb, e1 = x.je[1] - x.jb;
+    for (int32_t i = 0; i + 1 < n && go; ++i) {
+      go = wait(&sh.full[g % kAtPairs], g / kAtPairs & 1u);
+      const bool fresh = i % kAtChunkTiles == 0, end = (i + 1) % kAtChunkTiles == 0;
+#pragma unroll
+      for (int X = 0; X < 2; ++X) {
+        const int32_t e = X ? e1 : e0;
+        if (go && i < e) {
+          go = values(X, fresh);
+          if (end || i + 1 == e) umma_commit(&sh.o_full[X]);
+        }
+        if (i + 1 < e) {
+          scores(X);
+          if (i + 2 == e) umma_commit(&sh.q_empty[X]);
+        }
+      }
+      turn();
+    }
+    if (!go || !wait(&sh.full[g % kAtPairs], g / kAtPairs & 1u)) break;
+    if (x.ragged(x.n - 1)) {
+      const uint32_t b = g % kAtPairs;
+      if (!wait(&sh.z_full[b], (zph >> b) & 1u)) break;
+      zph ^= 1u << b;
+    }
+#pragma unroll
+    for (int X = 0; X < 2; ++X)
+      if (go && (X ? e1 : e0) == n) {
+        go = values(X, (n - 1) % kAtChunkTiles == 0);
+        umma_commit(&sh.o_full[X]);
+      }
+    if (go && next) go = first(nx);
+    turn();
   }
   umma_commit(&sh.done);
   mbar_wait<false>(&sh.done, 0u, wc);
@@ -742,8 +759,8 @@ __global__ void __launch_bounds__(kAtFwdThreads, 1)
   AtFwdShared& sh = *reinterpret_cast<AtFwdShared*>(dsmem + AtFwdTile<D>::smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 8; ++i) {
-      mbar_init(&sh.full[i], 1);
+    for (int i = 0; i < static_cast<int>(kAtPairs); ++i) {
+      mbar_init(&sh.full[i], 2);
       mbar_init(&sh.empty[i], 1);
       mbar_init(&sh.z_ask[i], 1);
       mbar_init(&sh.z_full[i], 1);
