@@ -24,6 +24,7 @@
 
 #include <cuda_runtime.h>
 #include <cstdint>
+#include <type_traits>
 
 #include "kernels_lm.cuh"
 
@@ -323,9 +324,10 @@ struct AtUnit {
   int32_t h;        // key/value head
   int32_t t0;
   int32_t jb;       // first key tile
-  int32_t je[2];    // end of each row tile's key tiles
+  int32_t je0, je1;  // end of each row tile's key tiles
   int32_t n;        // end of the unit's
   __device__ __forceinline__ int32_t tiles() const { return n > jb ? n - jb : 0; }
+  __device__ __forceinline__ int32_t je(int X) const { return X ? je1 : je0; }
   __device__ __forceinline__ bool ragged(int32_t j) const { return q.lk - j * kAtTile < kAtTile; }
   __device__ __forceinline__ void fetch(const AttnFwdArgs& a, int64_t u) {
     const AttnUnit w = a.units[u / a.Hkv];
@@ -333,15 +335,15 @@ struct AtUnit {
     q = a.seqs[w.seq];
     t0 = w.t0;
     jb = w.c0 * kAtChunkTiles;
-#pragma unroll
-    for (int X = 0; X < 2; ++X) {
-      const int32_t first = w.t0 + X * a.tpt;
-      int32_t last = first + a.tpt;
-      last = (last < q.lq ? last : q.lq) - 1;
-      const int32_t m = last < first ? 0 : (attn_visible(last, q.lq, q.lk, a.causal) + kAtTile - 1) / kAtTile;
-      je[X] = m < w.c1 * kAtChunkTiles ? m : w.c1 * kAtChunkTiles;
-    }
-    n = je[0] > je[1] ? je[0] : je[1];
+    const int32_t cap = w.c1 * kAtChunkTiles;
+    auto end = [&](int32_t from) {
+      const int32_t last = (from + a.tpt < q.lq ? from + a.tpt : q.lq) - 1;
+      const int32_t m = last < from ? 0 : (attn_visible(last, q.lq, q.lk, a.causal) + kAtTile - 1) / kAtTile;
+      return m < cap ? m : cap;
+    };
+    je0 = end(t0);
+    je1 = end(t0 + a.tpt);
+    n = je0 > je1 ? je0 : je1;
   }
 };
 
@@ -384,7 +386,7 @@ __device__ __forceinline__ void at_fwd_load(AtFwdShared& sh, const AttnFwdArgs& 
   tma_prefetch_desc(mv);
   const uint32_t ring = smem + 2 * T::tile_bytes;
   const uint32_t qbytes = static_cast<uint32_t>(a.tpt * a.G) * 128u * (D / 64);
-  uint32_t qph[2] = {0, 0}, g = 0;
+  uint32_t qph = 0, g = 0;
   // tile `pos` of the ring (keys of tile g at 2 g, values at 2 g + 1), for pair `pair`
   auto load = [&](uint32_t pos, uint32_t pair, const CUtensorMap* m, int32_t h, int32_t row) {
     if (pos >= T::slots) {
@@ -405,9 +407,9 @@ __device__ __forceinline__ void at_fwd_load(AtFwdShared& sh, const AttnFwdArgs& 
     if (walk.i == 1) {
 #pragma unroll
       for (int X = 0; X < 2; ++X) {
-        if (x.je[X] <= x.jb) continue;
-        if (!mbar_wait<false>(&sh.q_empty[X], qph[X] ^ 1u, wc)) return;
-        qph[X] ^= 1u;
+        if (x.je(X) <= x.jb) continue;
+        if (!mbar_wait<false>(&sh.q_empty[X], (qph >> X & 1u) ^ 1u, wc)) return;
+        qph ^= 1u << X;
         mbar_arrive_expect_tx(&sh.q_full[X], qbytes);
 #pragma unroll
         for (int b = 0; b < D / 64; ++b)
@@ -474,14 +476,17 @@ __device__ __forceinline__ void at_fwd_mma(AtFwdShared& sh, const AttnFwdArgs& a
   const uint64_t dq0 = sdesc_k_sw128(smem);
   const uint64_t dk0 = sdesc_k_sw128(smem + 2 * T::tile_bytes);
   const uint64_t dv0 = sdesc_mn_sw128(smem + 2 * T::tile_bytes, kAUnitBytes);
+  using Row0 = std::integral_constant<int, 0>;
+  using Row1 = std::integral_constant<int, 1>;
   uint32_t g = 0, kat = 0, vat = 0;      // pair; its tiles' slots times the tile's size
-  uint32_t qph[2] = {0, 0}, pph[2] = {0, 0}, zph = 0;
+  uint32_t qph = 0, pph = 0, zph = 0;    // a phase for each row tile; for each pair of barriers
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     const bool ok = mbar_wait<false>(bar, parity, wc);
     tc_fence_after();
     return ok;
   };
-  auto scores = [&](int X) {  // S_X = Q_X K^T
+  auto scores = [&](auto XC) {  // S_X = Q_X K^T
+    constexpr int X = decltype(XC)::value;
     const uint64_t da = dq0 + X * ts, db = dk0 + kat;
 #pragma unroll
     for (int b = 0; b < D / 64; ++b)
@@ -490,29 +495,29 @@ __device__ __forceinline__ void at_fwd_mma(AtFwdShared& sh, const AttnFwdArgs& a
         umma_bf16(tmem + X * 128, da + b * blk + 2 * k, db + b * blk + 2 * k, idesc_s, (b | k) ? 1u : 0u);
     umma_commit(&sh.s_full[X]);
   };
-  auto values = [&](int X, bool fresh) {  // O_X += P_X V
+  auto values = [&](auto XC, bool fresh) {  // O_X += P_X V
+    constexpr int X = decltype(XC)::value;
     const uint64_t db = dv0 + vat;
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-      if (!wait(&sh.p_full[X][half], pph[X])) return false;
+      if (!wait(&sh.p_full[X][half], pph >> X & 1u)) return false;
 #pragma unroll
       for (int k = 4 * half; k < 4 * half + 4; ++k)
         umma_bf16_ta(tmem + 256 + X * D, tmem + X * 128 + k * 8, db + k * (2048 >> 4), idesc_o, (k > 0 || !fresh) ? 1u : 0u);
     }
-    pph[X] ^= 1u;
+    pph ^= 1u << X;
     return true;
   };
-  auto first = [&](const AtUnit& x) {  // a unit's first scores
-#pragma unroll
-    for (int X = 0; X < 2; ++X)
-      if (x.je[X] > x.jb) {
-        if (!wait(&sh.q_full[X], qph[X])) return false;
-        qph[X] ^= 1u;
-        scores(X);
-        if (x.je[X] == x.jb + 1) umma_commit(&sh.q_empty[X]);
-      }
+  auto first1 = [&](const AtUnit& x, auto XC) {  // a unit's first scores
+    constexpr int X = decltype(XC)::value;
+    if (x.je(X) <= x.jb) return true;
+    if (!wait(&sh.q_full[X], qph >> X & 1u)) return false;
+    qph ^= 1u << X;
+    scores(XC);
+    if (x.je(X) == x.jb + 1) umma_commit(&sh.q_empty[X]);
     return true;
   };
+  auto first = [&](const AtUnit& x) { return first1(x, Row0{}) && first1(x, Row1{}); };
   auto turn = [&]() {  // on to the next pair
     umma_commit(&sh.empty[g % kAtPairs]);
     ++g;
@@ -535,22 +540,23 @@ __device__ __forceinline__ void at_fwd_mma(AtFwdShared& sh, const AttnFwdArgs& a
   while (go && next) {
     x = nx;
     next = fetch();
-    const int32_t n = x.n - x.jb, e0 = x.je[0] - x.jb, e1 = x.je[1] - x.jb;
+    const int32_t n = x.n - x.jb, e0 = x.je0 - x.jb, e1 = x.je1 - x.jb;
     for (int32_t i = 0; i + 1 < n && go; ++i) {
       go = wait(&sh.full[g % kAtPairs], g / kAtPairs & 1u);
       const bool fresh = i % kAtChunkTiles == 0, end = (i + 1) % kAtChunkTiles == 0;
-#pragma unroll
-      for (int X = 0; X < 2; ++X) {
-        const int32_t e = X ? e1 : e0;
-        if (go && i < e) {
-          go = values(X, fresh);
+      auto row = [&](auto XC, int32_t e) {
+        constexpr int X = decltype(XC)::value;
+        if (i < e) {
+          go = go && values(XC, fresh);
           if (end || i + 1 == e) umma_commit(&sh.o_full[X]);
         }
         if (i + 1 < e) {
-          scores(X);
+          scores(XC);
           if (i + 2 == e) umma_commit(&sh.q_empty[X]);
         }
-      }
+      };
+      row(Row0{}, e0);
+      row(Row1{}, e1);
       turn();
     }
     if (!go || !wait(&sh.full[g % kAtPairs], g / kAtPairs & 1u)) break;
@@ -559,12 +565,14 @@ __device__ __forceinline__ void at_fwd_mma(AtFwdShared& sh, const AttnFwdArgs& a
       if (!wait(&sh.z_full[b], (zph >> b) & 1u)) break;
       zph ^= 1u << b;
     }
-#pragma unroll
-    for (int X = 0; X < 2; ++X)
-      if (go && (X ? e1 : e0) == n) {
-        go = values(X, (n - 1) % kAtChunkTiles == 0);
-        umma_commit(&sh.o_full[X]);
-      }
+    auto row = [&](auto XC, int32_t e) {
+      constexpr int X = decltype(XC)::value;
+      if (e != n) return;
+      go = go && values(XC, (n - 1) % kAtChunkTiles == 0);
+      umma_commit(&sh.o_full[X]);
+    };
+    row(Row0{}, e0);
+    row(Row1{}, e1);
     if (go && next) go = first(nx);
     turn();
   }
@@ -597,7 +605,7 @@ __device__ __forceinline__ void at_fwd_softmax(AtFwdShared& sh, const AttnFwdArg
     uint16_t* out = a.out + ((x.q.q0 + tok) * a.Hq + head) * D;
     float* lse = a.lse + static_cast<int64_t>(head) * a.Tq + x.q.q0 + tok;
     const bool joined = split && x.q.nch > 1;  // k_attn_join writes the rows of this sequence
-    if (x.je[X] <= x.jb) {
+    if (x.je(X) <= x.jb) {
       if (valid && !joined) {  // no key to see
 #pragma unroll
         for (int e = 0; e < D / 8; ++e) reinterpret_cast<uint4*>(out)[e] = make_uint4(0u, 0u, 0u, 0u);
@@ -607,7 +615,7 @@ __device__ __forceinline__ void at_fwd_softmax(AtFwdShared& sh, const AttnFwdArg
     }
     float m = -INFINITY, l = 0.f;          // of the chunk
     float m_run = -INFINITY, l_run = 0.f;  // of the chunks before
-    for (int32_t j = x.jb; j < x.je[X]; ++j) {
+    for (int32_t j = x.jb; j < x.je(X); ++j) {
       if (!at_wait(&sh.s_full[X], sph, wc)) return;
       sph ^= 1u;
       const bool first = j % kAtChunkTiles == 0;
@@ -684,7 +692,7 @@ __device__ __forceinline__ void at_fwd_softmax(AtFwdShared& sh, const AttnFwdArg
         mbar_arrive(&sh.p_full[X][0]);
         mbar_arrive(&sh.p_full[X][1]);
       }
-      const bool last = j + 1 == x.je[X];
+      const bool last = j + 1 == x.je(X);
       if (!last && (j + 1) % kAtChunkTiles != 0) continue;
       // the chunk's end
       if (!at_wait(&sh.o_full[X], oph, wc)) return;
