@@ -50,7 +50,7 @@ FwdLayout fwd_layout(const Shape& z) {
     const int64_t most = static_cast<int64_t>(kPartBytesMax) / row;
     L.cap_part = want < most ? want : most;
   }
-  L.cap_units = static_cast<int32_t>(S + z.Tq / (2 * z.tpt) + 1 + L.cap_part);
+  L.cap_units = static_cast<int32_t>(S + z.Tq / z.tpt + 1 + L.cap_part);
   size_t o = 0;
   auto take = [&](size_t bytes) {
     const size_t at = o;
@@ -107,6 +107,12 @@ bool make_map_heads(CUtensorMap* m, const void* base, int64_t T, int32_t heads, 
            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+template <int D, int kRows>
+bool grant_fwd() {
+  return cudaFuncSetAttribute(bi::k_attn_fwd<D, kRows>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              bi::AtFwdTile<D, kRows>::smem + bi::kAtSharedBytes) == cudaSuccess;
+}
+
 // The current device's SM count, with the kernels' shared memory granted once.
 int attn_device() {
   static std::mutex mu;
@@ -123,22 +129,20 @@ int attn_device() {
         cudaFuncSetAttribute(bi::k_attn_dkv<64>, kSmem, bwd64) != cudaSuccess ||
         cudaFuncSetAttribute(bi::k_attn_dq<128>, kSmem, bwd128) != cudaSuccess ||
         cudaFuncSetAttribute(bi::k_attn_dq<64>, kSmem, bwd64) != cudaSuccess ||
-        cudaFuncSetAttribute(bi::k_attn_fwd<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             bi::AtFwdTile<128>::smem + bi::kAtSharedBytes) != cudaSuccess ||
-        cudaFuncSetAttribute(bi::k_attn_fwd<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             bi::AtFwdTile<64>::smem + bi::kAtSharedBytes) != cudaSuccess)
+        !grant_fwd<128, 1>() || !grant_fwd<128, 2>() || !grant_fwd<64, 1>() || !grant_fwd<64, 2>())
       return 0;
     ready[dev] = 1;
   }
   return sms;
 }
 
-template <int D>
+template <int D, int kRows>
 bool launch_fwd(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const bi::AttnFwdArgs& a,
                 unsigned grid, bool join, int32_t S, int sms, cudaStream_t s) {
   {
     ProfScope ps(kKAttnFwd, s);
-    bi::k_attn_fwd<D><<<grid, bi::kAtFwdThreads, bi::AtFwdTile<D>::smem + bi::kAtSharedBytes, s>>>(mq, mk, mv, a);
+    using T = bi::AtFwdTile<D, kRows>;
+    bi::k_attn_fwd<D, kRows><<<grid, T::threads, T::smem + bi::kAtSharedBytes, s>>>(mq, mk, mv, a);
   }
   if (join) {
     const int64_t want = (a.Tq * a.Hq + bi::kAtJoinThreads / 32 - 1) / (bi::kAtJoinThreads / 32);
@@ -208,9 +212,12 @@ bi_status bi_attn_fwd(const uint16_t* q, const uint16_t* k, const uint16_t* v, i
   p.S = S;
   p.mode = bi::kPlanFwd;
   p.causal = causal != 0;
-  p.step = 2 * z.tpt;
+  // one row tile a unit where the sequences' queries fill one at most on average (a decode step)
+  const int rows = Tq <= static_cast<int64_t>(S) * z.tpt ? 1 : 2;
+  const int blocks = rows == 1 ? 2 * sms : sms;
+  p.step = rows * z.tpt;
   p.tpt = z.tpt;
-  p.sms = sms;
+  p.sms = blocks;
   p.Hkv = Hkv;
   p.cap_units = L.cap_units;
   p.cap_part = L.cap_part;
@@ -244,14 +251,16 @@ bi_status bi_attn_fwd(const uint16_t* q, const uint16_t* k, const uint16_t* v, i
   a.Hkv = Hkv;
   a.G = z.G;
   a.tpt = z.tpt;
+  a.rows = rows;
   a.causal = p.causal;
   a.c = scale * bi::kLog2e;
   a.status = dev_status;
   a.limit_ns = kWaitLimitNs;
   const int64_t most = static_cast<int64_t>(L.cap_units) * Hkv;
-  const unsigned grid = static_cast<unsigned>(most < sms ? most : sms);
-  const bool ok = D == 128 ? launch_fwd<128>(mq, mk, mv, a, grid, L.cap_part > 0, S, sms, s)
-                           : launch_fwd<64>(mq, mk, mv, a, grid, L.cap_part > 0, S, sms, s);
+  const unsigned grid = static_cast<unsigned>(most < blocks ? most : blocks);
+  const auto go = D == 128 ? (rows == 1 ? launch_fwd<128, 1> : launch_fwd<128, 2>)
+                           : (rows == 1 ? launch_fwd<64, 1> : launch_fwd<64, 2>);
+  const bool ok = go(mq, mk, mv, a, grid, L.cap_part > 0, S, sms, s);
   return ok ? BI_OK : BI_ERR_CUDA;
 }
 

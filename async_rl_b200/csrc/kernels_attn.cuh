@@ -120,6 +120,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_attn_plan(const AttnPlanArgs p
   const AttnPlanArgs& a = blockIdx.x == 0 ? p0 : p1;
   __shared__ int64_t warp_sums[32];
   __shared__ int32_t hist[kPlanThreads];
+  __shared__ int32_t sh_unit0[kPlanThreads], sh_lq[kPlanThreads], sh_lk[kPlanThreads];  // S <= kPlanThreads
   __shared__ int32_t longest;
   __shared__ unsigned long long work;
   const int tid = threadIdx.x;
@@ -165,6 +166,11 @@ __global__ void __launch_bounds__(kPlanThreads) k_attn_plan(const AttnPlanArgs p
       q.unit0 = static_cast<int32_t>(en);
       q.part0 = ep;
       a.seqs[s] = q;
+      if (base == 0) {
+        sh_unit0[tid] = q.unit0;
+        sh_lq[tid] = q.lq;
+        sh_lk[tid] = q.lk;
+      }
     }
     units += tn;
     parts += tp;
@@ -183,6 +189,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_attn_plan(const AttnPlanArgs p
   // other SMs would wait for it.  It costs a write and a read of the partial rows.
   const bool split = a.mode == kPlanFwd && parts > 0 && parts <= a.cap_part && split_units <= a.cap_units &&
                      2ull * static_cast<unsigned long long>(longest) * a.sms > work * static_cast<unsigned long long>(a.Hkv);
+  const bool near = a.S <= kPlanThreads;
   // counting sort by cost, dearest first; the order within a cost is free (it decides which SM
   // works on a unit, never a result)
   for (int pass = 0; pass < 2; ++pass) {
@@ -190,14 +197,15 @@ __global__ void __launch_bounds__(kPlanThreads) k_attn_plan(const AttnPlanArgs p
       int32_t lo = 0, hi = a.S - 1;
       while (lo < hi) {  // the last sequence whose first unit is not behind i
         const int32_t mid = lo + (hi - lo + 1) / 2;
-        if (a.seqs[mid].unit0 <= i)
+        if ((near ? sh_unit0[mid] : a.seqs[mid].unit0) <= i)
           lo = mid;
         else
           hi = mid - 1;
       }
-      const AttnSeq& q = a.seqs[lo];
-      const int32_t t0 = static_cast<int32_t>(i - q.unit0) * a.step;
-      const int32_t cost = attn_cost(a, q.lq, q.lk, t0);
+      const int32_t unit0 = near ? sh_unit0[lo] : a.seqs[lo].unit0;
+      const int32_t lq = near ? sh_lq[lo] : a.seqs[lo].lq, lk = near ? sh_lk[lo] : a.seqs[lo].lk;
+      const int32_t t0 = static_cast<int32_t>(i - unit0) * a.step;
+      const int32_t cost = attn_cost(a, lq, lk, t0);
       const int32_t nc = split ? (cost + kAtChunkTiles - 1) / kAtChunkTiles : 1;
       for (int32_t c = 0; c < (nc > 0 ? nc : 1); ++c) {
         const int32_t left = cost - c * kAtChunkTiles;
@@ -233,29 +241,32 @@ struct AttnFwdArgs {
   const AttnPlanHead* head;
   uint16_t* out;       // [Tq][Hq][D]
   float* lse;          // [Hq][Tq]
-  float* scratch;      // [CTAs][2][D / 4][128][4]: running O of tiles with several chunks
+  float* scratch;      // [CTAs][rows][D / 4][128][4]: running O of tiles with several chunks
   float* part;         // [partial rows][Hq][D]
   float2* part_ml;     // [partial rows][Hq]: (m, l)
   int64_t Tq;
   int32_t Hq, Hkv, G, tpt;
+  int32_t rows;        // row tiles of a unit
   int32_t causal;
   float c;             // scale log2(e)
   int32_t* status;
   uint64_t limit_ns;
 };
 
-// Warps 0-3 and 4-7: softmax of the two row tiles, a row to a thread; 8: TMA; 9: MMA; 10: ragged value tiles.
-// A row's 128 scores stay in registers: the last four warps give up some of theirs
-// (2 x 208 + 88 = 3 x 168, what the block is launched with).
-constexpr int kAtFwdThreads = 384;
-constexpr int kAtFwdSoft = 8;
-constexpr int kAtSoftRegs = 208, kAtOtherRegs = 88;
-
-template <int D>
+// kRows: row tiles of a unit.  Two share every key tile, and one's products run beside the other's softmax;
+// single tokens fill one only, and two blocks of one row tile then share an SM.
+// Warps 0-3 (and 4-7): softmax of the row tiles, a row to a thread; then TMA, MMA and ragged value tiles.
+// A row's 128 scores stay in registers: the last four warps give up some of theirs (2 x 208 + 88 = 3 x 168
+// and 168 + 88 = 2 x 128, what the block is launched with).
+template <int D, int kRows>
 struct AtFwdTile {
   static constexpr int tile_bytes = kAtTile * D * 2;       // Q, K and V tiles: D / 64 blocks of [128][64]
-  static constexpr int slots = D == 128 ? 5 : 12;          // ring of K and V tiles
-  static constexpr int smem = (2 + slots) * tile_bytes;
+  static constexpr int slots = kRows == 2 ? (D == 128 ? 5 : 12) : (D == 128 ? 2 : 5);  // ring of K and V tiles
+  static constexpr int smem = (kRows + slots) * tile_bytes;
+  static constexpr int soft = 4 * kRows;                   // warps
+  static constexpr int threads = 128 * kRows + 128;
+  static constexpr int soft_regs = kRows == 2 ? 208 : 168, other_regs = 88;
+  static constexpr int tmem = 256 * kRows;                 // columns: S of each row tile, then O
 };
 constexpr uint32_t kAtPairs = 8;    // more than a ring of tiles can hold
 struct AtFwdShared {
@@ -342,7 +353,7 @@ struct AtUnit {
       return m < cap ? m : cap;
     };
     je0 = end(t0);
-    je1 = end(t0 + a.tpt);
+    je1 = a.rows == 2 ? end(t0 + a.tpt) : 0;
     n = je0 > je1 ? je0 : je1;
   }
 };
@@ -376,15 +387,15 @@ struct AtWalk {
   }
 };
 
-template <int D>
+template <int D, int kRows>
 __device__ __forceinline__ void at_fwd_load(AtFwdShared& sh, const AttnFwdArgs& a, uint32_t smem, int64_t nu,
                                             const CUtensorMap* mq, const CUtensorMap* mk, const CUtensorMap* mv) {
-  using T = AtFwdTile<D>;
+  using T = AtFwdTile<D, kRows>;
   const WaitCtl wc{&sh.abort_flag, a.status, a.limit_ns};
   tma_prefetch_desc(mq);
   tma_prefetch_desc(mk);
   tma_prefetch_desc(mv);
-  const uint32_t ring = smem + 2 * T::tile_bytes;
+  const uint32_t ring = smem + kRows * T::tile_bytes;
   const uint32_t qbytes = static_cast<uint32_t>(a.tpt * a.G) * 128u * (D / 64);
   uint32_t qph = 0, g = 0;
   // tile `pos` of the ring (keys of tile g at 2 g, values at 2 g + 1), for pair `pair`
@@ -406,7 +417,7 @@ __device__ __forceinline__ void at_fwd_load(AtFwdShared& sh, const AttnFwdArgs& 
     const int32_t j = x.jb + walk.i - 1;
     if (walk.i == 1) {
 #pragma unroll
-      for (int X = 0; X < 2; ++X) {
+      for (int X = 0; X < kRows; ++X) {
         if (x.je(X) <= x.jb) continue;
         if (!mbar_wait<false>(&sh.q_empty[X], (qph >> X & 1u) ^ 1u, wc)) return;
         qph ^= 1u << X;
@@ -441,9 +452,9 @@ __device__ __forceinline__ void at_zero_rows(uint8_t* tile, int valid) {
 
 // Value rows behind a sequence's last key, before the products see them.  The loading thread asks with the
 // tile's load; until the tile is used up its slot, and with it the pair of barriers, belongs to it.
-template <int D>
+template <int D, int kRows>
 __device__ __forceinline__ void at_fwd_ragged(AtFwdShared& sh, const AttnFwdArgs& a, uint8_t* smem_p, int64_t nu) {
-  using T = AtFwdTile<D>;
+  using T = AtFwdTile<D, kRows>;
   const WaitCtl wc{&sh.abort_flag, a.status, a.limit_ns};
   uint32_t g = 0, used = 0;  // the unit's first tile, a phase for each pair of barriers
   for (int64_t r = 0, u; (u = at_turn(r)) < nu; ++r) {
@@ -456,7 +467,7 @@ __device__ __forceinline__ void at_fwd_ragged(AtFwdShared& sh, const AttnFwdArgs
     const uint32_t b = g % kAtPairs;
     if (!at_wait(&sh.z_ask[b], (used >> b) & 1u, wc) || !at_wait(&sh.full[b], g / kAtPairs & 1u, wc)) return;
     used ^= 1u << b;
-    at_zero_rows<D>(smem_p + (2 + (2 * g - 1) % T::slots) * T::tile_bytes, x.q.lk - (x.n - 1) * kAtTile);
+    at_zero_rows<D>(smem_p + (kRows + (2 * g - 1) % T::slots) * T::tile_bytes, x.q.lk - (x.n - 1) * kAtTile);
     if ((threadIdx.x & 31) == 0) mbar_arrive(&sh.z_full[b]);
   }
 }
@@ -464,18 +475,18 @@ __device__ __forceinline__ void at_fwd_ragged(AtFwdShared& sh, const AttnFwdArgs
 // One thread.  A row tile's next scores go behind its product with the values, into the columns that held
 // its P; the other row tile's softmax runs meanwhile.  The loop over a unit's tiles is kept short: what the
 // thread does besides issuing has to fit into the time of 32 MMAs, 2048 clocks.
-template <int D>
+template <int D, int kRows>
 __device__ __forceinline__ void at_fwd_mma(AtFwdShared& sh, const AttnFwdArgs& a, uint32_t smem, int64_t nu,
                                            uint32_t tmem) {
-  using T = AtFwdTile<D>;
+  using T = AtFwdTile<D, kRows>;
   const WaitCtl wc{&sh.abort_flag, a.status, a.limit_ns};
   constexpr uint32_t idesc_s = idesc_bf16(128, 128, false, false);
   constexpr uint32_t idesc_o = idesc_bf16(128, D, false, true);
   constexpr uint64_t blk = kAUnitBytes >> 4;
   constexpr uint32_t ts = T::tile_bytes >> 4;
   const uint64_t dq0 = sdesc_k_sw128(smem);
-  const uint64_t dk0 = sdesc_k_sw128(smem + 2 * T::tile_bytes);
-  const uint64_t dv0 = sdesc_mn_sw128(smem + 2 * T::tile_bytes, kAUnitBytes);
+  const uint64_t dk0 = sdesc_k_sw128(smem + kRows * T::tile_bytes);
+  const uint64_t dv0 = sdesc_mn_sw128(smem + kRows * T::tile_bytes, kAUnitBytes);
   using Row0 = std::integral_constant<int, 0>;
   using Row1 = std::integral_constant<int, 1>;
   uint32_t g = 0, kat = 0, vat = 0;      // pair; its tiles' slots times the tile's size
@@ -503,7 +514,7 @@ __device__ __forceinline__ void at_fwd_mma(AtFwdShared& sh, const AttnFwdArgs& a
       if (!wait(&sh.p_full[X][half], pph >> X & 1u)) return false;
 #pragma unroll
       for (int k = 4 * half; k < 4 * half + 4; ++k)
-        umma_bf16_ta(tmem + 256 + X * D, tmem + X * 128 + k * 8, db + k * (2048 >> 4), idesc_o, (k > 0 || !fresh) ? 1u : 0u);
+        umma_bf16_ta(tmem + 128 * kRows + X * D, tmem + X * 128 + k * 8, db + k * (2048 >> 4), idesc_o, (k > 0 || !fresh) ? 1u : 0u);
     }
     pph ^= 1u << X;
     return true;
@@ -517,7 +528,7 @@ __device__ __forceinline__ void at_fwd_mma(AtFwdShared& sh, const AttnFwdArgs& a
     if (x.je(X) == x.jb + 1) umma_commit(&sh.q_empty[X]);
     return true;
   };
-  auto first = [&](const AtUnit& x) { return first1(x, Row0{}) && first1(x, Row1{}); };
+  auto first = [&](const AtUnit& x) { return first1(x, Row0{}) && (kRows == 1 || first1(x, Row1{})); };
   auto turn = [&]() {  // on to the next pair
     umma_commit(&sh.empty[g % kAtPairs]);
     ++g;
@@ -556,7 +567,7 @@ __device__ __forceinline__ void at_fwd_mma(AtFwdShared& sh, const AttnFwdArgs& a
         }
       };
       row(Row0{}, e0);
-      row(Row1{}, e1);
+      if (kRows == 2) row(Row1{}, e1);
       turn();
     }
     if (!go || !wait(&sh.full[g % kAtPairs], g / kAtPairs & 1u)) break;
@@ -572,7 +583,7 @@ __device__ __forceinline__ void at_fwd_mma(AtFwdShared& sh, const AttnFwdArgs& a
       umma_commit(&sh.o_full[X]);
     };
     row(Row0{}, e0);
-    row(Row1{}, e1);
+    if (kRows == 2) row(Row1{}, e1);
     if (go && next) go = first(nx);
     turn();
   }
@@ -581,16 +592,16 @@ __device__ __forceinline__ void at_fwd_mma(AtFwdShared& sh, const AttnFwdArgs& a
 }
 
 // Softmax and output of row tile X (128 threads, a row each).
-template <int D>
+template <int D, int kRows>
 __device__ __forceinline__ void at_fwd_softmax(AtFwdShared& sh, const AttnFwdArgs& a, int X, int64_t nu, bool split,
                                                uint32_t tmem) {
   const WaitCtl wc{&sh.abort_flag, a.status, a.limit_ns};
   const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
   const int row = warp * 32 + lane;
   const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
-  const uint32_t ts = tmem + X * 128 + lanes, to = tmem + 256 + X * D + lanes;
+  const uint32_t ts = tmem + X * 128 + lanes, to = tmem + 128 * kRows + X * D + lanes;
   const int tok_in = row / a.G, g = row - tok_in * a.G;
-  float4* scr = reinterpret_cast<float4*>(a.scratch) + ((static_cast<int64_t>(blockIdx.x) * 2 + X) * (D / 4)) * 128 + row;
+  float4* scr = reinterpret_cast<float4*>(a.scratch) + ((static_cast<int64_t>(blockIdx.x) * kRows + X) * (D / 4)) * 128 + row;
   uint32_t sph = 0, oph = 0;
   const float2 cc = make_float2(a.c, a.c);
   for (int64_t r = 0, u; (u = at_turn(r)) < nu; ++r) {
@@ -758,13 +769,14 @@ __device__ __forceinline__ void at_fwd_softmax(AtFwdShared& sh, const AttnFwdArg
   }
 }
 
-template <int D>
-__global__ void __launch_bounds__(kAtFwdThreads, 1)
+template <int D, int kRows>
+__global__ void __launch_bounds__(AtFwdTile<D, kRows>::threads, 3 - kRows)
     k_attn_fwd(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                const __grid_constant__ CUtensorMap mv, const AttnFwdArgs a) {
   // mq: Q [Tq][Hq][D], box {64, G, tpt}; mk, mv: [Tk][Hkv][D], box {64, 1, 128}; 128-byte swizzle
+  using T = AtFwdTile<D, kRows>;
   extern __shared__ __align__(1024) uint8_t dsmem[];
-  AtFwdShared& sh = *reinterpret_cast<AtFwdShared*>(dsmem + AtFwdTile<D>::smem);
+  AtFwdShared& sh = *reinterpret_cast<AtFwdShared*>(dsmem + T::smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < static_cast<int>(kAtPairs); ++i) {
@@ -785,8 +797,8 @@ __global__ void __launch_bounds__(kAtFwdThreads, 1)
     sh.abort_flag = 0u;
     fence_mbar_init_cluster();
   }
-  if (warp == kAtFwdSoft + 1) {
-    tmem_alloc(&sh.tmem_base, 512);
+  if (warp == T::soft + 1) {
+    tmem_alloc(&sh.tmem_base, T::tmem);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -798,19 +810,19 @@ __global__ void __launch_bounds__(kAtFwdThreads, 1)
   if (misaligned && threadIdx.x == 0) raise_status(a.status, 4 /* BI_ERR_CUDA */);
   const int64_t nu = misaligned ? 0 : static_cast<int64_t>(a.head->nunits) * a.Hkv;
   const bool split = a.head->split != 0;
-  if (warp < kAtFwdSoft) {
-    regs_take<kAtSoftRegs>();
-    at_fwd_softmax<D>(sh, a, warp >> 2, nu, split, tmem);
+  if (warp < T::soft) {
+    regs_take<T::soft_regs>();
+    at_fwd_softmax<D, kRows>(sh, a, warp >> 2, nu, split, tmem);
   } else {
-    regs_give<kAtOtherRegs>();
-    if (warp == kAtFwdSoft) {
-      if (lane == 0) at_fwd_load<D>(sh, a, smem, nu, &mq, &mk, &mv);
+    regs_give<T::other_regs>();
+    if (warp == T::soft) {
+      if (lane == 0) at_fwd_load<D, kRows>(sh, a, smem, nu, &mq, &mk, &mv);
       __syncwarp();
-    } else if (warp == kAtFwdSoft + 1) {
-      if (elect_one()) at_fwd_mma<D>(sh, a, smem, nu, tmem);
+    } else if (warp == T::soft + 1) {
+      if (elect_one()) at_fwd_mma<D, kRows>(sh, a, smem, nu, tmem);
       __syncwarp();
-    } else if (warp == kAtFwdSoft + 2) {
-      at_fwd_ragged<D>(sh, a, dsmem, nu);
+    } else if (warp == T::soft + 2) {
+      at_fwd_ragged<D, kRows>(sh, a, dsmem, nu);
     }
   }
   tc_fence_before();
@@ -820,9 +832,9 @@ __global__ void __launch_bounds__(kAtFwdThreads, 1)
     while (globaltimer_ns() - t0 < 50000u) {
     }
   }
-  if (warp == kAtFwdSoft + 1) {
+  if (warp == T::soft + 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(tmem, T::tmem);
   }
 }
 
