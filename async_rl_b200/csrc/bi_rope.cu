@@ -24,22 +24,22 @@ int lanes_of(int32_t D) {
 }
 
 // A warp takes a token with all its heads, so that its angles are computed once, where the tokens
-// alone fill the SMs; with fewer tokens it takes as many heads as fit in one pass, so that a
-// decode step's few tokens do not queue their heads one behind another.
+// alone fill the SMs; with fewer tokens it takes one pass's heads, so that a decode step's few tokens
+// do not queue their heads one behind another.
 void split_heads(bi::RopeArgs& a, int lh, int sms) {
-  const int nh = a.Hq + a.Hkv, at_once = 32 / lh;
-  a.hb = a.T >= static_cast<int64_t>(sms) * 16 ? nh : at_once;
-  a.nhb = (nh + a.hb - 1) / a.hb;
+  const int at_once = 32 / lh;
+  const int slots = (a.Hq + at_once - 1) / at_once + (a.Hkv + at_once - 1) / at_once;
+  a.sb = a.T >= static_cast<int64_t>(sms) * 16 ? slots : 1;
+  a.nsb = (slots + a.sb - 1) / a.sb;
 }
 
 unsigned grid_of(const bi::RopeArgs& a, int sms, int per_sm) {
-  const int64_t items = a.T * a.nhb;
+  const int64_t items = a.T * a.nsb;
   const int64_t want = (items + bi::kRopeWarps - 1) / bi::kRopeWarps;
   const int64_t cap = static_cast<int64_t>(sms) * per_sm;
   return static_cast<unsigned>(want < cap ? want : cap);
 }
 
-constexpr int kFwdBlocksPerSm = 4;
 constexpr int kBwdBlocksPerSm = 2;
 constexpr int kMaxSms = 160;
 
@@ -89,7 +89,7 @@ bi_status bi_qk_norm_rope(const uint16_t* q, const uint16_t* k, int64_t q_ld, in
   a.status = dev_status;
   const int lh = lanes_of(D);
   split_heads(a, lh, sms);
-  const unsigned grid = grid_of(a, sms, kFwdBlocksPerSm);
+  const unsigned grid = grid_of(a, sms, bi::kRopeFwdBlocks);
   ProfScope ps(kKQkRope, s);
 #define BI_ROPE(LH_)                                                                   \
   if (lh == LH_) {                                                                     \
