@@ -88,21 +88,28 @@ __device__ __forceinline__ void adam_st_bf16(uint16_t* p, const F8& f) {
   *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(f.x[0], f.x[1]), pack_bf16x2(f.x[2], f.x[3]),
                                             pack_bf16x2(f.x[4], f.x[5]), pack_bf16x2(f.x[6], f.x[7]));
 }
-__device__ __forceinline__ float e4m3_up(uint32_t code) {
-  const __half_raw h = __nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(code), __NV_E4M3);
-  return __half2float(__half(h));
+// Eight e4m3 codes, two at a time (a code is exact in fp16), and back (to nearest even, saturated).
+__device__ __forceinline__ void e4m3_up8(const uint32_t (&w)[2], float (&x)[8]) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w[e / 2] >> (16 * (e % 2))), __NV_E4M3);
+    const float2 f = __half22float2(__half2(h));
+    x[2 * e] = f.x;
+    x[2 * e + 1] = f.y;
+  }
 }
-__device__ __forceinline__ uint32_t e4m3_down(float x) {
-  return __nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3);
+__device__ __forceinline__ uint32_t e4m3_down2(float lo, float hi) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
 }
 
 // One element; every operation is rounded, none contracted, so a plain evaluation in the same order
 // gives the same bits (and with 8-bit states the same codes).
-__device__ __forceinline__ void adam_one(const AdamHyper& h, float gs, float g, float& p, float& m, float& v) {
+__device__ __forceinline__ void adam_one(const AdamHyper& h, float gs, float g, float& p, float& m, float& v, float& root) {
   g = __fmul_rn(g, gs);  // gs = 1 without a grad_scale: exact
   m = __fadd_rn(__fmul_rn(m, h.b1), __fmul_rn(g, h.c1));
   v = __fadd_rn(__fmul_rn(v, h.b2), __fmul_rn(__fmul_rn(g, g), h.c2));
-  const float den = __fadd_rn(__fmul_rn(__fsqrt_rn(v), h.root), h.eps);
+  root = __fsqrt_rn(v);
+  const float den = __fadd_rn(__fmul_rn(root, h.root), h.eps);
   p = __fsub_rn(__fmul_rn(p, h.keep), __fdiv_rn(__fmul_rn(m, h.rate), den));
 }
 
@@ -151,69 +158,82 @@ __global__ void __launch_bounds__(kAdamThreads) k_adamw(const __grid_constant__ 
   uint16_t* pb = static_cast<uint16_t*>(t.p);
   const float* gf = static_cast<const float*>(t.g);
   const uint16_t* gb = static_cast<const uint16_t*>(t.g);
-#pragma unroll
-  for (int u = 0; u < kAdamUnitsPerWarp; ++u) {
-    const int64_t unit = base + static_cast<int64_t>(u) * (kAdamThreads / 32) * kAdamUnit;
-    const int64_t i0 = unit + lane * 8;
-    if (unit >= n) break;  // the whole warp
-    const bool full = wide && i0 + 8 <= n;
+  // What a lane holds of a unit.  With 8-bit states, whose arithmetic takes as long as their bytes, the
+  // loads of both units are in flight together (430 -> ADAM8_US us on 109 million elements).
+  struct Held {
     F8 p, g, m, v;
-    const int64_t block = unit / kAdamUnit;
-    if (full) {
-      g = kGBf16 ? adam_ld_bf16(gb + i0) : adam_ld_f32(gf + i0);
-      p = (kPBf16 && !kMaster) ? adam_ld_bf16(pb + i0) : adam_ld_f32(pf + i0);
+    uint32_t mw[2], vw[2];
+    float sm, sv;
+  };
+  auto unit_of = [&](int u) { return base + static_cast<int64_t>(u) * (kAdamThreads / 32) * kAdamUnit; };
+  auto load = [&](int u, Held& x) {
+    const int64_t unit = unit_of(u), i0 = unit + lane * 8;
+    if (unit >= n) return;
+    if (wide && i0 + 8 <= n) {
+      x.g = kGBf16 ? adam_ld_bf16(gb + i0) : adam_ld_f32(gf + i0);
+      x.p = (kPBf16 && !kMaster) ? adam_ld_bf16(pb + i0) : adam_ld_f32(pf + i0);
       if (!kState8) {
-        m = adam_ld_f32(static_cast<const float*>(t.m) + i0);
-        v = adam_ld_f32(static_cast<const float*>(t.v) + i0);
+        x.m = adam_ld_f32(static_cast<const float*>(t.m) + i0);
+        x.v = adam_ld_f32(static_cast<const float*>(t.v) + i0);
       }
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const int64_t i = i0 + e;
         const bool in = i < n;
-        g.x[e] = !in ? 0.f : kGBf16 ? bf16_up(gb[i]) : gf[i];
-        p.x[e] = !in ? 0.f : (kPBf16 && !kMaster) ? bf16_up(pb[i]) : pf[i];
+        x.g.x[e] = !in ? 0.f : kGBf16 ? bf16_up(gb[i]) : gf[i];
+        x.p.x[e] = !in ? 0.f : (kPBf16 && !kMaster) ? bf16_up(pb[i]) : pf[i];
         if (!kState8) {
-          m.x[e] = in ? static_cast<const float*>(t.m)[i] : 0.f;
-          v.x[e] = in ? static_cast<const float*>(t.v)[i] : 0.f;
+          x.m.x[e] = in ? static_cast<const float*>(t.m)[i] : 0.f;
+          x.v.x[e] = in ? static_cast<const float*>(t.v)[i] : 0.f;
         }
       }
     }
     if (kState8) {
       const uint8_t* mc = static_cast<const uint8_t*>(t.m) + i0;
       const uint8_t* vc = static_cast<const uint8_t*>(t.v) + i0;
-      uint32_t mw[2] = {}, vw[2] = {};
-      if (full) {
-        const uint2 x = *reinterpret_cast<const uint2*>(mc), y = *reinterpret_cast<const uint2*>(vc);
-        mw[0] = x.x, mw[1] = x.y, vw[0] = y.x, vw[1] = y.y;
+      x.mw[0] = x.mw[1] = x.vw[0] = x.vw[1] = 0u;
+      if (wide && i0 + 8 <= n) {
+        const uint2 a2 = *reinterpret_cast<const uint2*>(mc), b2 = *reinterpret_cast<const uint2*>(vc);
+        x.mw[0] = a2.x, x.mw[1] = a2.y, x.vw[0] = b2.x, x.vw[1] = b2.y;
       } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
           if (i0 + e < n) {
-            mw[e / 4] |= static_cast<uint32_t>(mc[e]) << (8 * (e % 4));
-            vw[e / 4] |= static_cast<uint32_t>(vc[e]) << (8 * (e % 4));
+            x.mw[e / 4] |= static_cast<uint32_t>(mc[e]) << (8 * (e % 4));
+            x.vw[e / 4] |= static_cast<uint32_t>(vc[e]) << (8 * (e % 4));
           }
       }
-      const float sm = t.ms[block], sv = t.vs[block];
+      const int64_t block = unit / kAdamUnit;
+      x.sm = t.ms[block];
+      x.sv = t.vs[block];
+    }
+  };
+  auto work = [&](int u, Held& x) {
+    const int64_t unit = unit_of(u), i0 = unit + lane * 8;
+    if (unit >= n) return;  // the whole warp
+    const bool full = wide && i0 + 8 <= n;
+    if (kState8) {
+      e4m3_up8(x.mw, x.m.x);
+      e4m3_up8(x.vw, x.v.x);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        m.x[e] = __fmul_rn(e4m3_up((mw[e / 4] >> (8 * (e % 4))) & 0xffu), sm);
-        const float r = __fmul_rn(e4m3_up((vw[e / 4] >> (8 * (e % 4))) & 0xffu), sv);
-        v.x[e] = __fmul_rn(r, r);
+        x.m.x[e] = __fmul_rn(x.m.x[e], x.sm);
+        const float r = __fmul_rn(x.v.x[e], x.sv);
+        x.v.x[e] = __fmul_rn(r, r);
       }
     }
+    float root[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) adam_one(h, gs, g.x[e], p.x[e], m.x[e], v.x[e]);
+    for (int e = 0; e < 8; ++e) adam_one(h, gs, x.g.x[e], x.p.x[e], x.m.x[e], x.v.x[e], root[e]);
     if (kState8) {
       float mm = 0.f, mv = 0.f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        v.x[e] = __fsqrt_rn(v.x[e]);
+      for (int e = 0; e < 8; ++e)
         if (i0 + e < n) {
-          mm = fmaxf(mm, fabsf(m.x[e]));
-          mv = fmaxf(mv, v.x[e]);
+          mm = fmaxf(mm, fabsf(x.m.x[e]));
+          mv = fmaxf(mv, root[e]);
         }
-      }
       mm = adam_warp_max(mm);
       mv = adam_warp_max(mv);
       // a subnormal maximum's reciprocal would be infinite; sqrt(v) is never that small
@@ -222,10 +242,14 @@ __global__ void __launch_bounds__(kAdamThreads) k_adamw(const __grid_constant__ 
       uint32_t mw[2] = {}, vw[2] = {};
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        float r = __fmul_rn(v.x[e], iv);
-        if (v.x[e] > 0.f) r = fmaxf(r, kE4m3Tiny);
-        mw[e / 4] |= e4m3_down(__fmul_rn(m.x[e], im)) << (8 * (e % 4));
-        vw[e / 4] |= e4m3_down(r) << (8 * (e % 4));
+        const float r = __fmul_rn(root[e], iv);
+        root[e] = root[e] > 0.f ? fmaxf(r, kE4m3Tiny) : r;
+        x.m.x[e] = __fmul_rn(x.m.x[e], im);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; e += 2) {
+        mw[e / 4] |= e4m3_down2(x.m.x[e], x.m.x[e + 1]) << (8 * (e % 4));
+        vw[e / 4] |= e4m3_down2(root[e], root[e + 1]) << (8 * (e % 4));
       }
       uint8_t* mc = static_cast<uint8_t*>(t.m) + i0;
       uint8_t* vc = static_cast<uint8_t*>(t.v) + i0;
@@ -241,31 +265,39 @@ __global__ void __launch_bounds__(kAdamThreads) k_adamw(const __grid_constant__ 
           }
       }
       if (lane == 0) {
+        const int64_t block = unit / kAdamUnit;
         t.ms[block] = __fmul_rn(mm, kE4m3Inv);
         t.vs[block] = __fmul_rn(mv, kE4m3Inv);
       }
     }
     if (full) {
-      if (kPBf16) adam_st_bf16(pb + i0, p);
-      if (!kPBf16 || kMaster) adam_st_f32(pf + i0, p);
+      if (kPBf16) adam_st_bf16(pb + i0, x.p);
+      if (!kPBf16 || kMaster) adam_st_f32(pf + i0, x.p);
       if (!kState8) {
-        adam_st_f32(static_cast<float*>(t.m) + i0, m);
-        adam_st_f32(static_cast<float*>(t.v) + i0, v);
+        adam_st_f32(static_cast<float*>(t.m) + i0, x.m);
+        adam_st_f32(static_cast<float*>(t.v) + i0, x.v);
       }
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const int64_t i = i0 + e;
         if (i >= n) continue;
-        if (kPBf16) pb[i] = static_cast<uint16_t>(pack_bf16x2(p.x[e], 0.f) & 0xffffu);
-        if (!kPBf16 || kMaster) pf[i] = p.x[e];
+        if (kPBf16) pb[i] = static_cast<uint16_t>(pack_bf16x2(x.p.x[e], 0.f) & 0xffffu);
+        if (!kPBf16 || kMaster) pf[i] = x.p.x[e];
         if (!kState8) {
-          static_cast<float*>(t.m)[i] = m.x[e];
-          static_cast<float*>(t.v)[i] = v.x[e];
+          static_cast<float*>(t.m)[i] = x.m.x[e];
+          static_cast<float*>(t.v)[i] = x.v.x[e];
         }
       }
     }
-  }
+  };
+  static_assert(kAdamUnitsPerWarp == 2, "two units");
+  Held x0, x1;
+  load(0, x0);
+  if (kState8) load(1, x1);
+  work(0, x0);
+  if (!kState8) load(1, x1);
+  work(1, x1);
 }
 
 }  // namespace bi
