@@ -19,8 +19,7 @@ namespace bi {
 
 constexpr int kAdamThreads = 256;
 constexpr int kAdamUnit = 256;                      // elements of a warp's turn = a block of 8-bit states
-constexpr int kAdamUnitsPerWarp = 2;
-constexpr int kAdamChunk = kAdamUnit * kAdamUnitsPerWarp * (kAdamThreads / 32);  // elements of a block
+constexpr int kAdamChunk = kAdamUnit * (kAdamThreads / 32);  // elements of a block
 constexpr float kE4m3Max = 448.0f;
 constexpr float kE4m3Inv = 1.0f / 448.0f;
 constexpr float kE4m3Tiny = 0.001953125f;           // 2^-9, the smallest positive value
@@ -121,7 +120,7 @@ __device__ __forceinline__ float adam_warp_max(float v) {
 
 // kState8: 8-bit states; kPBf16: bf16 params; kMaster: with fp32 masters; kGBf16: bf16 gradients
 template <int kMax, bool kState8, bool kPBf16, bool kMaster, bool kGBf16>
-__global__ void __launch_bounds__(kAdamThreads) k_adamw(const __grid_constant__ AdamTable<kMax> tab, const AdamArgs a) {
+__global__ void __launch_bounds__(kAdamThreads, kState8 ? 6 : 3) k_adamw(const __grid_constant__ AdamTable<kMax> tab, const AdamArgs a) {
   __shared__ AdamHyper sh;
   AdamHyper h = a.h;
   if (a.step_dev) {
@@ -153,22 +152,22 @@ __global__ void __launch_bounds__(kAdamThreads) k_adamw(const __grid_constant__ 
   const bool wide = (tab.wide[lo / 32] >> (lo % 32)) & 1u;
   const int64_t n = t.n;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t base = static_cast<int64_t>(blockIdx.x - tab.first[lo]) * kAdamChunk + warp * kAdamUnit;
+  const int64_t unit = static_cast<int64_t>(blockIdx.x - tab.first[lo]) * kAdamChunk + warp * kAdamUnit;
+  const int64_t i0 = unit + lane * 8;
+  if (unit >= n) return;  // the whole warp
   float* pf = kMaster ? t.master : static_cast<float*>(t.p);
   uint16_t* pb = static_cast<uint16_t*>(t.p);
   const float* gf = static_cast<const float*>(t.g);
   const uint16_t* gb = static_cast<const uint16_t*>(t.g);
-  // What a lane holds of a unit.  With 8-bit states, whose arithmetic takes as long as their bytes, the
-  // loads of both units are in flight together (430 -> ADAM8_US us on 109 million elements).
+  // What a lane holds.  One unit a warp and, with 8-bit states, six blocks an SM: their step is bound by
+  // the latency of its chain of conversions, roots and quotients, which warps hide better than loads ahead
+  // (110 million elements, bf16 gradients, masters: 342 us; two units with both loads ahead 413, four blocks 382).
   struct Held {
     F8 p, g, m, v;
     uint32_t mw[2], vw[2];
     float sm, sv;
   };
-  auto unit_of = [&](int u) { return base + static_cast<int64_t>(u) * (kAdamThreads / 32) * kAdamUnit; };
-  auto load = [&](int u, Held& x) {
-    const int64_t unit = unit_of(u), i0 = unit + lane * 8;
-    if (unit >= n) return;
+  auto load = [&](Held& x) {
     if (wide && i0 + 8 <= n) {
       x.g = kGBf16 ? adam_ld_bf16(gb + i0) : adam_ld_f32(gf + i0);
       x.p = (kPBf16 && !kMaster) ? adam_ld_bf16(pb + i0) : adam_ld_f32(pf + i0);
@@ -209,9 +208,7 @@ __global__ void __launch_bounds__(kAdamThreads) k_adamw(const __grid_constant__ 
       x.sv = t.vs[block];
     }
   };
-  auto work = [&](int u, Held& x) {
-    const int64_t unit = unit_of(u), i0 = unit + lane * 8;
-    if (unit >= n) return;  // the whole warp
+  auto work = [&](Held& x) {
     const bool full = wide && i0 + 8 <= n;
     if (kState8) {
       e4m3_up8(x.mw, x.m.x);
@@ -291,13 +288,9 @@ __global__ void __launch_bounds__(kAdamThreads) k_adamw(const __grid_constant__ 
       }
     }
   };
-  static_assert(kAdamUnitsPerWarp == 2, "two units");
-  Held x0, x1;
-  load(0, x0);
-  if (kState8) load(1, x1);
-  work(0, x0);
-  if (!kState8) load(1, x1);
-  work(1, x1);
+  Held x;
+  load(x);
+  work(x);
 }
 
 }  // namespace bi
