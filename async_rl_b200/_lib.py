@@ -28,13 +28,6 @@ class LossCfg(ctypes.Structure):
                 ("gate", ctypes.c_float), ("flags", ctypes.c_int32)]
 
 
-class AdamWTensor(ctypes.Structure):
-    """bi_adamw_tensor"""
-    _fields_ = [("param", ctypes.c_void_p), ("master", ctypes.c_void_p), ("grad", ctypes.c_void_p),
-                ("exp_avg", ctypes.c_void_p), ("exp_avg_sq", ctypes.c_void_p), ("exp_avg_scale", ctypes.c_void_p),
-                ("exp_avg_sq_scale", ctypes.c_void_p), ("n", ctypes.c_int64)]
-
-
 class AdamWCfg(ctypes.Structure):
     """bi_adamw_cfg"""
     _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),

@@ -26,7 +26,8 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 
 
 def _stream(device: torch.device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+    # the handle alone: building a Stream object takes longer than the rest of a small call
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if device.index is None else device.index)
 
 
 def _check_cuda(t: torch.Tensor, name: str, dtype: torch.dtype, device: torch.device):

@@ -34,6 +34,11 @@ def _need(t: torch.Tensor, name: str, dtype: torch.dtype, dev: torch.device, sha
 
 def _rows(t: torch.Tensor, name: str, dev: torch.device, shape=None) -> int:
     """Elements between the tokens of a [T, heads, D] bf16 tensor whose heads are contiguous."""
+    if t.get_device() == dev.index and t.dtype is torch.bfloat16 and t.dim() == 3 and shape in (None, t.shape):
+        T, H, D = t.shape
+        ld, sh, sd = t.stride()
+        if T > 1 and sd == 1 and sh == D:  # what nearly every call has
+            return ld
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor, got {t.device}")
     if t.device != dev:

@@ -4,6 +4,7 @@ from __future__ import annotations
 import ctypes
 from typing import List, Optional, Sequence, Union
 
+import numpy as np
 import torch
 
 from . import _lib
@@ -33,12 +34,16 @@ class AdamWState:
     ``params``: float32 or bfloat16, all of one type.  ``masters``: float32 weights of bfloat16 params
     (the update is made there and rounded into the param), or None.  ``exp_avg``, ``exp_avg_sq``:
     float32, or float8_e4m3fn with ``exp_avg_scale`` and ``exp_avg_sq_scale`` (float32, one for each
-    256 elements): then m = exp_avg * scale and sqrt(v) = exp_avg_sq * scale."""
+    256 elements): then m = exp_avg * scale and sqrt(v) = exp_avg_sq * scale.  A tensor whose storage is
+    replaced (``param.data = ...``) is checked anew at the next step."""
 
     def __init__(self, params: Sequence[torch.Tensor], masters: Optional[Sequence[torch.Tensor]],
                  exp_avg: Sequence[torch.Tensor], exp_avg_sq: Sequence[torch.Tensor],
                  exp_avg_scale: Optional[Sequence[torch.Tensor]] = None,
                  exp_avg_sq_scale: Optional[Sequence[torch.Tensor]] = None):
+        self._bind(params, masters, exp_avg, exp_avg_sq, exp_avg_scale, exp_avg_sq_scale)
+
+    def _bind(self, params, masters, exp_avg, exp_avg_sq, exp_avg_scale, exp_avg_sq_scale):
         n = len(params)
         if n == 0:
             raise ValueError("params is empty")
@@ -71,6 +76,24 @@ class AdamWState:
         for (_, end), (start, _) in zip(spans, spans[1:]):
             if start < end:
                 raise ValueError("the tensors of one step may not overlap")
+        # the rows of bi_adamw_tensor; the gradients' addresses are filled in at each step
+        self._flat = self.tensors()
+        self._ptrs = [t.data_ptr() for t in self._flat]
+        columns = (self.params, self.masters, None, self.exp_avg, self.exp_avg_sq, self.exp_avg_scale,
+                   self.exp_avg_sq_scale)
+        self._table = np.zeros((n, 8), dtype=np.int64)
+        for i, ts in enumerate(columns):
+            if ts is not None:
+                self._table[:, i] = [t.data_ptr() for t in ts]
+        self._table[:, 7] = self.sizes
+
+    def _rows(self, grads: Sequence[torch.Tensor]) -> np.ndarray:
+        """The step's table; tensors that moved since the last one are checked again."""
+        if [t.data_ptr() for t in self._flat] != self._ptrs:
+            self._bind(self.params, self.masters, self.exp_avg, self.exp_avg_sq, self.exp_avg_scale,
+                       self.exp_avg_sq_scale)
+        self._table[:, 2] = [g.data_ptr() for g in grads]
+        return self._table
 
     @staticmethod
     def allocate(params: Sequence[torch.Tensor], state_bits: int = 32, master: bool = False) -> "AdamWState":
@@ -104,8 +127,9 @@ def adamw_step(state: AdamWState, grads: Sequence[torch.Tensor], step: Union[int
     gt = grads[0].dtype
     if gt not in (torch.float32, torch.bfloat16):
         raise ValueError(f"grads must be float32 or bfloat16, got {gt}")
+    index = dev.index
     for i, (g, shape) in enumerate(zip(grads, state.shapes)):
-        if not g.is_cuda or g.device != dev or g.dtype != gt or g.shape != shape or not g.is_contiguous():
+        if g.dtype is not gt or g.get_device() != index or g.shape != shape or not g.is_contiguous():
             raise ValueError(f"grads[{i}] must be a contiguous {gt} CUDA tensor of shape {list(shape)} on {dev}, got "
                              f"{g.dtype} {list(g.shape)} on {g.device}")
     step_dev = None
@@ -117,14 +141,11 @@ def adamw_step(state: AdamWState, grads: Sequence[torch.Tensor], step: Union[int
                                    grad_scale.dtype != torch.float32 or grad_scale.numel() != 1):
         raise ValueError(f"grad_scale must be a CUDA float32 tensor of one element on {dev}")
     st = _status(status, dev)
-    ptrs = lambda ts: (0,) * n if ts is None else [t.data_ptr() for t in ts]  # noqa: E731
-    table = (_lib.AdamWTensor * n)(*zip(ptrs(state.params), ptrs(state.masters), ptrs(grads), ptrs(state.exp_avg),
-                                        ptrs(state.exp_avg_sq), ptrs(state.exp_avg_scale),
-                                        ptrs(state.exp_avg_sq_scale), state.sizes))
+    table = state._rows(grads)
     cfg = _lib.AdamWCfg(float(lr), float(beta1), float(beta2), float(eps), float(weight_decay), int(step),
                         state.state_bits, int(state.param_bf16), int(gt == torch.bfloat16), 0)
     with _on(dev):
-        code = _lib.load().bi_adamw_step(ctypes.addressof(table), n, ctypes.addressof(cfg), _ptr(grad_scale),
+        code = _lib.load().bi_adamw_step(table.ctypes.data, n, ctypes.addressof(cfg), _ptr(grad_scale),
                                          _ptr(step_dev), _ptr(st), _stream(dev))
     _raise_host(code, "bi_adamw_step")
     return st

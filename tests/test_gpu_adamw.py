@@ -263,3 +263,20 @@ def test_allocated_state_and_refusals(cuda_device):
         bi.adamw_step(st, g, 0, 1e-3)
     with pytest.raises(bi.BiError):
         bi.adamw_step(st, g, 1, 1e-3, beta1=1.0)
+
+
+def test_a_replaced_storage_is_followed(cuda_device):
+    """``param.data = ...`` between two steps: the new storage is updated, the old one left alone; one of
+    another size or type is refused."""
+    d = _make([300, 1000], torch.float32, False, torch.float32, 32, seed=5)
+    st, g = _state(d, cuda_device)
+    old = st.params[1].data
+    fresh = old.clone()
+    st.params[1].data = fresh
+    kept = old.clone()
+    bi.check_status(bi.adamw_step(st, g, 3, **HYPER))
+    assert torch.equal(old, kept) and st.params[1].data_ptr() == fresh.data_ptr()
+    _check(d, st, 3)
+    st.params[0].data = torch.zeros(299, device=cuda_device)
+    with pytest.raises(ValueError):
+        bi.adamw_step(st, g, 4, **HYPER)
