@@ -731,6 +731,27 @@ __device__ __forceinline__ void at_fwd_softmax(AtFwdShared& sh, const AttnFwdArg
       l_run = fresh ? l : fmaf(l, kb, l_run * ka);
       m_run = m_new;
       const float inv = l_run > 0.f || l_run != l_run ? 1.f / l_run : 0.f;
+      if (fresh && last) {  // a row of one chunk: all of O at once
+        uint32_t o[D / 32][32];
+#pragma unroll
+        for (int b = 0; b < D / 32; ++b) tmem_ld32(to + b * 32, o[b]);
+        tmem_ld_wait();
+#pragma unroll
+        for (int b = 0; b < D / 32; ++b) {
+          tmem_ld_pin(o[b]);
+          uint32_t p[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            p[e] = pack_bf16x2(__uint_as_float(o[b][2 * e]) * inv, __uint_as_float(o[b][2 * e + 1]) * inv);
+          if (valid)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              *reinterpret_cast<uint4*>(out + b * 32 + e * 8) =
+                  make_uint4(p[4 * e], p[4 * e + 1], p[4 * e + 2], p[4 * e + 3]);
+        }
+        if (valid) *lse = m_run == -INFINITY ? -INFINITY : fmaf(m_run, 0.69314718055994531f, logf(l_run));
+        continue;
+      }
 #pragma unroll 1
       for (int b = 0; b < D / 32; ++b) {
         uint32_t o[32];
