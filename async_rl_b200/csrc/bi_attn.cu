@@ -194,7 +194,8 @@ bi_status bi_attn_fwd(const uint16_t* q, const uint16_t* k, const uint16_t* v, i
   if (!dev_status || !sizes_ok(z) || !(scale > 0.f) || !std::isfinite(scale)) return BI_ERR_INVALID_ARG;
   if (!shape_ok(z)) return BI_ERR_UNSUPPORTED_SHAPE;
   if (S > 0 && (!q_offsets || !k_offsets)) return BI_ERR_INVALID_ARG;
-  if (Tq > 0 && (!rows_ok(q, q_ld, Hq, D) || !out || !aligned16(out) || !lse)) return BI_ERR_INVALID_ARG;
+  if (Tq > 0 && (!rows_ok(q, q_ld, Hq, D) || !out || !aligned16(out) || !lse || out == q || out == k || out == v))
+    return BI_ERR_INVALID_ARG;
   if (Tk > 0 && (!rows_ok(k, k_ld, Hkv, D) || !rows_ok(v, v_ld, Hkv, D))) return BI_ERR_INVALID_ARG;
   const FwdLayout L = fwd_layout(z);
   if (!ws || ws_bytes < L.total || (reinterpret_cast<uintptr_t>(ws) & 255u)) return BI_ERR_WORKSPACE;

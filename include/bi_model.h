@@ -121,6 +121,8 @@ BI_API bi_status bi_qk_norm_rope_bwd(const uint16_t* dq_out, const uint16_t* dk_
  * queries (prefill) or alone over a cache (decode).  A NaN or infinity in a key or value row of a sequence
  * reaches every query of that sequence that shares a 128-row tile with one that sees it.
  * The terms of the softmax are rounded to bf16 for the product with v; sums, maxima and lse are fp32.
+ * out may not overlap an input.  ws belongs to the call until its kernels end: calls (and graphs) that may
+ * run at the same time need one each.
  * Device status: BI_ERR_BAD_OFFSETS (offsets that decrease or leave the tensors, k_lens below 0 or past the
  * next offset): nothing is written then.  Returns BI_ERR_WORKSPACE for a ws below
  * bi_attn_fwd_workspace_bytes(...) bytes or not 256-byte aligned, and the codes of the entry points above.

@@ -201,3 +201,38 @@ def test_streams_and_a_graph_with_new_lengths(cuda_device):
         want = both()
         assert all(torch.equal(a, b) for a, b in zip(held, want))
         bi.check_status(held[3])
+
+
+def test_many_short_sequences(cuda_device):
+    """More sequences than the plan's threads, most of them empty or a few tokens long, forward and backward."""
+    from tests.test_gpu_attention import check_fwd
+    dev = cuda_device
+    gen = torch.Generator().manual_seed(1)
+    lens = torch.randint(0, 5, (2600,), generator=gen).tolist()
+    lens[7], lens[2599] = 300, 150
+    Hq, Hkv, D = 3, 1, 64
+    T = sum(lens)
+    q, k, v, dout = _rand(T, Hq, D, 1), _rand(T, Hkv, D, 2), _rand(T, Hkv, D, 3), _rand(T, Hq, D, 4)
+    o = _offs(lens)
+    t = [x.to(dev) for x in (q, k, v)]
+    out, lse, st = bi.attn_fwd(*t, o.to(dev))
+    bi.check_status(st)
+    check_fwd(q, k, v, ao.sequences(o), True, D ** -0.5, out, lse)
+    dq, dk, dv, st = bi.attn_bwd(dout.to(dev), *t, out, lse, o.to(dev))
+    bi.check_status(st)
+    check_bwd(q, k, v, dout, ao.sequences(o), True, D ** -0.5, dq, dk, dv)
+
+
+def test_one_query_over_a_long_cache(cuda_device):
+    """35 chunks of keys joined, and their gradients."""
+    from tests.test_gpu_attention import check_fwd
+    dev = cuda_device
+    q, k, v, dout = _rand(1, 4, 64, 1), _rand(70001, 1, 64, 2), _rand(70001, 1, 64, 3), _rand(1, 4, 64, 4)
+    qo, ko = torch.tensor([0, 1]), torch.tensor([0, 70001])
+    t = [x.to(dev) for x in (q, k, v)]
+    out, lse, st = bi.attn_fwd(*t, qo.to(dev), k_offsets=ko.to(dev))
+    bi.check_status(st)
+    check_fwd(q, k, v, ao.sequences(qo, ko), True, 64 ** -0.5, out, lse)
+    got = bi.attn_bwd(dout.to(dev), *t, out, lse, qo.to(dev), k_offsets=ko.to(dev))
+    bi.check_status(got[3])
+    check_bwd(q, k, v, dout, ao.sequences(qo, ko), True, 64 ** -0.5, *got[:3])

@@ -149,3 +149,12 @@ def test_decode_step_has_the_prefill_bits(Hq, Hkv, D, cuda_device):
                                k_lens=torch.tensor(lens, dtype=torch.int32, device=cuda_device))
     bi.check_status(st)
     assert _same(out, r["out"][last]) and torch.equal(lse, r["lse"][:, last])
+
+
+def test_a_process_may_capture_its_first_call(cuda_device):
+    import os
+    import subprocess
+    import sys
+    path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "capture_first_call.py")
+    p = subprocess.run([sys.executable, path], capture_output=True, text=True, timeout=120)
+    assert p.returncode == 0 and "captured first calls ok" in p.stdout, p.stderr[-2000:]

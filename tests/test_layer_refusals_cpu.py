@@ -65,7 +65,8 @@ COMMON = [
     (dict(q_ld=1000), ARG), (dict(out=None), ARG), (dict(lse=None), ARG), (dict(ws=None), WS), (dict(n=100), WS)]
 
 
-@pytest.mark.parametrize("change,code", COMMON + [(dict(ws=A[8] + 16), WS), (dict(out=A[5] + 2), ARG)])
+@pytest.mark.parametrize("change,code", COMMON + [(dict(ws=A[8] + 16), WS), (dict(out=A[5] + 2), ARG),
+                                                   (dict(out=A[0]), ARG), (dict(out=A[1]), ARG), (dict(out=A[2]), ARG)])
 def test_attn_fwd_refuses(lib, change, code):
     assert _call(lib.bi_attn_fwd, FWD, **change) == code
 
