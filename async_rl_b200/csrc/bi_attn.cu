@@ -256,6 +256,7 @@ bi_status bi_attn_fwd(const uint16_t* q, const uint16_t* k, const uint16_t* v, i
   a.causal = p.causal;
   a.c = scale * bi::kLog2e;
   a.status = dev_status;
+  a.wide = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
   a.limit_ns = kWaitLimitNs;
   const int64_t most = static_cast<int64_t>(L.cap_units) * Hkv;
   const unsigned grid = static_cast<unsigned>(most < blocks ? most : blocks);
@@ -357,7 +358,9 @@ bi_status bi_attn_bwd(const uint16_t* dout, int64_t dout_ld, const uint16_t* q, 
   a.scale = scale;
   a.status = dev_status;
   a.limit_ns = kWaitLimitNs;
+  a.wide = (reinterpret_cast<uintptr_t>(dq) & 31u) == 0 && dq_ld % 16 == 0;
   bi::AttnBwdArgs b = a;
+  b.wide = ((reinterpret_cast<uintptr_t>(dk) | reinterpret_cast<uintptr_t>(dv)) & 31u) == 0 && dk_ld % 16 == 0 && dv_ld % 16 == 0;
   b.seqs = pk.seqs;
   b.units = pk.units;
   b.head = pk.head;

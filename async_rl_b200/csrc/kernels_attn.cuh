@@ -249,6 +249,7 @@ struct AttnFwdArgs {
   int32_t rows;        // row tiles of a unit
   int32_t causal;
   float c;             // scale log2(e)
+  bool wide;           // out starts at a 32-byte boundary
   int32_t* status;
   uint64_t limit_ns;
 };
@@ -290,6 +291,16 @@ __device__ __forceinline__ float attn_join_scale(float from, float to) {
 // that began with a dear one ends with a cheap one.
 __device__ __forceinline__ int64_t at_turn(int64_t r) {
   return r * gridDim.x + ((r & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+}
+// 32 bytes of a row.  Lanes hold rows of their own, so a warp's store touches 32 lines whatever its width: one
+// wide store takes half the time of two.
+__device__ __forceinline__ void at_store32b(uint16_t* o, const uint32_t* w, bool wide) {
+  if (wide) {
+    st_global_v8(o, w);
+  } else {
+    reinterpret_cast<uint4*>(o)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4*>(o)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
 }
 // Keeps a rarely taken branch a branch: its selects are not to be executed everywhere.
 __device__ __forceinline__ void at_rare() { asm volatile("" ::: "memory"); }
@@ -743,11 +754,10 @@ __device__ __forceinline__ void at_fwd_softmax(AtFwdShared& sh, const AttnFwdArg
 #pragma unroll
           for (int e = 0; e < 16; ++e)
             p[e] = pack_bf16x2(__uint_as_float(o[b][2 * e]) * inv, __uint_as_float(o[b][2 * e + 1]) * inv);
-          if (valid)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              *reinterpret_cast<uint4*>(out + b * 32 + e * 8) =
-                  make_uint4(p[4 * e], p[4 * e + 1], p[4 * e + 2], p[4 * e + 3]);
+          if (valid) {
+            at_store32b(out + b * 32, p, a.wide);
+            at_store32b(out + b * 32 + 16, p + 8, a.wide);
+          }
         }
         if (valid) *lse = m_run == -INFINITY ? -INFINITY : fmaf(m_run, 0.69314718055994531f, logf(l_run));
         continue;

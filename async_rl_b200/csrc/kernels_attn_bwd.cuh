@@ -40,6 +40,7 @@ struct AttnBwdArgs {
   int32_t causal;
   float c;                     // scale log2(e)
   float scale;
+  bool wide;                   // rows of the outputs start at 32-byte boundaries
   int32_t* status;
   uint64_t limit_ns;
 };
@@ -234,7 +235,7 @@ __device__ __forceinline__ void at_put(uint32_t t, const float2 (&p)[8]) {
   tmem_st8(t, w);
 }
 // 16 columns of an accumulator, scaled, as bf16 (whole warp; stored where `valid`).
-__device__ __forceinline__ void at_store16(uint32_t t, float scale, uint16_t* o, bool valid) {
+__device__ __forceinline__ void at_store16(uint32_t t, float scale, uint16_t* o, bool valid, bool wide) {
   uint32_t s[16], w[8];
   tmem_ld16(t, s);
   tmem_ld_wait();
@@ -242,10 +243,7 @@ __device__ __forceinline__ void at_store16(uint32_t t, float scale, uint16_t* o,
 #pragma unroll
   for (int e = 0; e < 8; ++e)
     w[e] = pack_bf16x2(__uint_as_float(s[2 * e]) * scale, __uint_as_float(s[2 * e + 1]) * scale);
-  if (valid)
-#pragma unroll
-    for (int e = 0; e < 2; ++e)
-      reinterpret_cast<uint4*>(o)[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+  if (valid) at_store32b(o, w, wide);
 }
 __device__ __forceinline__ void at_zero16(uint16_t* o) {
 #pragma unroll
@@ -472,7 +470,7 @@ __device__ __forceinline__ void at_dkv_probs(AtBwdShared& sh, const AttnBwdArgs&
     if (!wait(&sh.acc_full, aph)) return false;
     aph ^= 1u;
 #pragma unroll 1
-    for (int b = 0; b < D / 32; ++b) at_store16(t_acc + b * 16, X < 2 ? a.scale : 1.f, done_o + b * 16, done_valid);
+    for (int b = 0; b < D / 32; ++b) at_store16(t_acc + b * 16, X < 2 ? a.scale : 1.f, done_o + b * 16, done_valid, a.wide);
     pending = false;
     return true;
   };
@@ -781,7 +779,7 @@ __device__ __forceinline__ void at_dq_probs(AtBwdShared& sh, const AttnBwdArgs& 
     aph ^= 1u;
 #pragma unroll
     for (int b = 0; b < D / 64; ++b)
-      at_store16(tmem + lanes + 384 + X * (D / 4) + b * 16, a.scale, done_o + b * 16, done_valid);
+      at_store16(tmem + lanes + 384 + X * (D / 4) + b * 16, a.scale, done_o + b * 16, done_valid, a.wide);
     pending = false;
     return true;
   };
