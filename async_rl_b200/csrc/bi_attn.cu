@@ -32,6 +32,12 @@ bool rows_ok(const void* p, int64_t ld, int32_t heads, int32_t D) {
   return p && aligned16(p) && ld >= static_cast<int64_t>(heads) * D && ld % 8 == 0;
 }
 
+// Some roles wait for the length of a unit, which passes over all keys or all query rows of a sequence: 40 ns
+// a key and row, four times what they take.
+uint64_t wait_limit(const Shape& z) {
+  return kWaitLimitNs + 40ull * static_cast<uint64_t>(z.Tk + z.Tq * z.G);
+}
+
 // Workspace of the forward.  Partial rows are provided where the rows alone would leave SMs without
 // work (fewer than four row tiles an SM), for sequences of up to twice the mean number of queries;
 // where that is not enough the plan does not split, and the results are the same.
@@ -257,7 +263,7 @@ bi_status bi_attn_fwd(const uint16_t* q, const uint16_t* k, const uint16_t* v, i
   a.c = scale * bi::kLog2e;
   a.status = dev_status;
   a.wide = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
-  a.limit_ns = kWaitLimitNs;
+  a.limit_ns = wait_limit(z);
   const int64_t most = static_cast<int64_t>(L.cap_units) * Hkv;
   const unsigned grid = static_cast<unsigned>(most < blocks ? most : blocks);
   const auto go = D == 128 ? (rows == 1 ? launch_fwd<128, 1> : launch_fwd<128, 2>)
@@ -357,7 +363,7 @@ bi_status bi_attn_bwd(const uint16_t* dout, int64_t dout_ld, const uint16_t* q, 
   a.c = scale * bi::kLog2e;
   a.scale = scale;
   a.status = dev_status;
-  a.limit_ns = kWaitLimitNs;
+  a.limit_ns = wait_limit(z);
   a.wide = (reinterpret_cast<uintptr_t>(dq) & 31u) == 0 && dq_ld % 16 == 0;
   bi::AttnBwdArgs b = a;
   b.wide = ((reinterpret_cast<uintptr_t>(dk) | reinterpret_cast<uintptr_t>(dv)) & 31u) == 0 && dk_ld % 16 == 0 && dv_ld % 16 == 0;
