@@ -137,14 +137,14 @@ __global__ void k_zero_prompt_rows(const int64_t* __restrict__ off, const int32_
 }
 
 // One warp per compact row: copy the scored hidden rows into the compact buffer and zero the rows
-// that pad the last 128-row tile.
+// that pad the last tile, of 128 rows or of NZ <= 256 (what lies there is multiplied by zeros, which
+// a NaN of an earlier use of the workspace survives).  Past T the tensor maps read zeros.
 __global__ void k_gather_rows(const uint16_t* __restrict__ hidden, int64_t T, int H, const Ctrl* ctrl,
                               const int32_t* __restrict__ rowmap, uint16_t* __restrict__ hc) {
   const int64_t k = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
   const int lane = threadIdx.x & 31;
   const int64_t ns = ctrl->n_scored;
-  const int64_t lim = ((ns + 127) / 128) * 128;
-  if (k >= T || k >= lim) return;
+  if (k >= T || k >= ns + 256) return;
   uint4* dst = reinterpret_cast<uint4*>(hc + k * H);
   if (k < ns) {
     const uint4* src = reinterpret_cast<const uint4*>(hidden + static_cast<int64_t>(rowmap[k]) * H);
