@@ -11,9 +11,10 @@ namespace {
 
 using namespace bi::host;
 
-// Tensors of one launch: the small table keeps a few tensors' launch short, the large one fills
+// Tensors of one launch: the small tables keep the launch of a few tensors short, the large one fills
 // the 32,764 bytes that kernel parameters may take.
 constexpr int kSmall = 16;
+constexpr int kMiddle = 96;
 constexpr int kLarge = 440;
 static_assert(sizeof(bi::AdamTable<kLarge>) + sizeof(bi::AdamArgs) <= 32764, "kernel parameters");
 
@@ -112,8 +113,9 @@ extern "C" bi_status bi_adamw_step(const bi_adamw_tensor* tensors, int32_t count
   a.set_status = 1;
   int32_t at = 0;
   while (at < count)
-    if (!(count - at <= kSmall ? launch<kSmall>(tensors, at, count, c, master, a, s)
-                              : launch<kLarge>(tensors, at, count, c, master, a, s)))
+    if (!(count - at <= kSmall    ? launch<kSmall>(tensors, at, count, c, master, a, s)
+          : count - at <= kMiddle ? launch<kMiddle>(tensors, at, count, c, master, a, s)
+                                  : launch<kLarge>(tensors, at, count, c, master, a, s)))
       return BI_ERR_CUDA;
   if (a.set_status && cudaMemsetAsync(dev_status, 0, sizeof(int32_t), s) != cudaSuccess) return BI_ERR_CUDA;
   return BI_OK;

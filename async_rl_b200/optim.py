@@ -89,10 +89,10 @@ class AdamWState:
 
     def _rows(self, grads: Sequence[torch.Tensor]) -> np.ndarray:
         """The step's table; tensors that moved since the last one are checked again."""
-        if [t.data_ptr() for t in self._flat] != self._ptrs:
+        if list(map(torch.Tensor.data_ptr, self._flat)) != self._ptrs:
             self._bind(self.params, self.masters, self.exp_avg, self.exp_avg_sq, self.exp_avg_scale,
                        self.exp_avg_sq_scale)
-        self._table[:, 2] = [g.data_ptr() for g in grads]
+        self._table[:, 2] = list(map(torch.Tensor.data_ptr, grads))
         return self._table
 
     @staticmethod
@@ -128,10 +128,13 @@ def adamw_step(state: AdamWState, grads: Sequence[torch.Tensor], step: Union[int
     if gt not in (torch.float32, torch.bfloat16):
         raise ValueError(f"grads must be float32 or bfloat16, got {gt}")
     index = dev.index
-    for i, (g, shape) in enumerate(zip(grads, state.shapes)):
-        if g.dtype is not gt or g.get_device() != index or g.shape != shape or not g.is_contiguous():
-            raise ValueError(f"grads[{i}] must be a contiguous {gt} CUDA tensor of shape {list(shape)} on {dev}, got "
-                             f"{g.dtype} {list(g.shape)} on {g.device}")
+    # whole lists at a time: with hundreds of small tensors the call is bound by these checks
+    if ([g.shape for g in grads] != state.shapes or {g.dtype for g in grads} != {gt} or
+            {g.get_device() for g in grads} != {index} or not all([g.is_contiguous() for g in grads])):
+        for i, (g, shape) in enumerate(zip(grads, state.shapes)):
+            if g.dtype is not gt or g.get_device() != index or g.shape != shape or not g.is_contiguous():
+                raise ValueError(f"grads[{i}] must be a contiguous {gt} CUDA tensor of shape {list(shape)} on {dev}, got "
+                                 f"{g.dtype} {list(g.shape)} on {g.device}")
     step_dev = None
     if isinstance(step, torch.Tensor):
         if not step.is_cuda or step.device != dev or step.dtype != torch.int64 or step.numel() != 1:

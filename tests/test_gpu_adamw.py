@@ -280,3 +280,11 @@ def test_a_replaced_storage_is_followed(cuda_device):
     st.params[0].data = torch.zeros(299, device=cuda_device)
     with pytest.raises(ValueError):
         bi.adamw_step(st, g, 4, **HYPER)
+
+
+@pytest.mark.parametrize("count", [16, 17, 96, 97, 440, 441])
+def test_as_many_tensors_as_a_launch_takes_and_one_more(count, cuda_device):
+    d = _make([1 + 7 * (i % 40) for i in range(count)], torch.bfloat16, True, torch.bfloat16, 8, seed=count)
+    st, g = _state(d, cuda_device)
+    bi.check_status(bi.adamw_step(st, g, 3, **HYPER))
+    _check(d, st, 3)
