@@ -332,11 +332,10 @@ __device__ __forceinline__ float2 ex2_poly(float2 x) {
 // 2^x of a pair of columns.  The special function unit gives 16 results a clock and SM, as long for a
 // tile's scores as its products take, so some columns of every 16 go to the FMA units instead; which
 // ones is a matter of the column alone, so a row's bits do not depend on its batch.
-#ifndef BI_AT_POLY
-#define BI_AT_POLY 0x94  // pairs 2, 4 and 7 of 8
-#endif
+// (None, 2, 3 or 4 of 8 pairs: dK, dV and dQ of 16 sequences take 467, 463, 458 and 473 us together.)
+constexpr uint32_t kAtPoly = 0x94;  // pairs 2, 4 and 7 of 8
 __device__ __forceinline__ float2 at_ex2(int pair, float2 x) {
-  if ((BI_AT_POLY >> (pair % 8)) & 1) return ex2_poly(x);
+  if ((kAtPoly >> (pair % 8)) & 1) return ex2_poly(x);
   return make_float2(ex2_approx(x.x), ex2_approx(x.y));
 }
 
