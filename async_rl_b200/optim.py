@@ -44,48 +44,47 @@ class AdamWState:
         self._bind(params, masters, exp_avg, exp_avg_sq, exp_avg_scale, exp_avg_sq_scale)
 
     def _bind(self, params, masters, exp_avg, exp_avg_sq, exp_avg_scale, exp_avg_sq_scale):
+        # into locals first: a handle that is bound again and refused stays what it was
         n = len(params)
         if n == 0:
             raise ValueError("params is empty")
-        self.device = params[0].device
+        device = params[0].device
         if params[0].dtype not in (torch.float32, torch.bfloat16):
             raise ValueError(f"params must be float32 or bfloat16, got {params[0].dtype}")
-        self.param_bf16 = params[0].dtype == torch.bfloat16
-        self.sizes = [p.numel() for p in params]
-        self.shapes = [p.shape for p in params]
-        _flat(params, "params", n, params[0].dtype, self.device)
+        param_bf16 = params[0].dtype == torch.bfloat16
+        sizes = [p.numel() for p in params]
+        _flat(params, "params", n, params[0].dtype, device)
         if masters is not None:
-            if not self.param_bf16:
+            if not param_bf16:
                 raise ValueError("masters are for bfloat16 params")
-            _flat(masters, "masters", n, torch.float32, self.device, self.sizes)
+            _flat(masters, "masters", n, torch.float32, device, sizes)
         if (exp_avg_scale is None) != (exp_avg_sq_scale is None):
             raise ValueError("exp_avg_scale and exp_avg_sq_scale are given together or not at all")
-        self.state_bits = 32 if exp_avg_scale is None else 8
-        held = torch.float32 if self.state_bits == 32 else torch.float8_e4m3fn
-        _flat(exp_avg, "exp_avg", n, held, self.device, self.sizes)
-        _flat(exp_avg_sq, "exp_avg_sq", n, held, self.device, self.sizes)
-        if self.state_bits == 8:
-            blocks = [-(-s // STATE_BLOCK) for s in self.sizes]
-            _flat(exp_avg_scale, "exp_avg_scale", n, torch.float32, self.device, blocks)
-            _flat(exp_avg_sq_scale, "exp_avg_sq_scale", n, torch.float32, self.device, blocks)
-        self.params, self.masters = list(params), None if masters is None else list(masters)
-        self.exp_avg, self.exp_avg_sq = list(exp_avg), list(exp_avg_sq)
-        self.exp_avg_scale = None if exp_avg_scale is None else list(exp_avg_scale)
-        self.exp_avg_sq_scale = None if exp_avg_sq_scale is None else list(exp_avg_sq_scale)
-        spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in self.tensors() if t.numel())
+        state_bits = 32 if exp_avg_scale is None else 8
+        held = torch.float32 if state_bits == 32 else torch.float8_e4m3fn
+        _flat(exp_avg, "exp_avg", n, held, device, sizes)
+        _flat(exp_avg_sq, "exp_avg_sq", n, held, device, sizes)
+        if state_bits == 8:
+            blocks = [-(-s // STATE_BLOCK) for s in sizes]
+            _flat(exp_avg_scale, "exp_avg_scale", n, torch.float32, device, blocks)
+            _flat(exp_avg_sq_scale, "exp_avg_sq_scale", n, torch.float32, device, blocks)
+        lists = [None if ts is None else list(ts)
+                 for ts in (params, masters, exp_avg, exp_avg_sq, exp_avg_scale, exp_avg_sq_scale)]
+        flat = [t for ts in lists if ts is not None for t in ts]
+        spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in flat if t.numel())
         for (_, end), (start, _) in zip(spans, spans[1:]):
             if start < end:
                 raise ValueError("the tensors of one step may not overlap")
         # the rows of bi_adamw_tensor; the gradients' addresses are filled in at each step
-        self._flat = self.tensors()
-        self._ptrs = [t.data_ptr() for t in self._flat]
-        columns = (self.params, self.masters, None, self.exp_avg, self.exp_avg_sq, self.exp_avg_scale,
-                   self.exp_avg_sq_scale)
-        self._table = np.zeros((n, 8), dtype=np.int64)
-        for i, ts in enumerate(columns):
+        table = np.zeros((n, 8), dtype=np.int64)
+        for i, ts in zip((0, 1, 3, 4, 5, 6), lists):
             if ts is not None:
-                self._table[:, i] = [t.data_ptr() for t in ts]
-        self._table[:, 7] = self.sizes
+                table[:, i] = [t.data_ptr() for t in ts]
+        table[:, 7] = sizes
+        self.device, self.param_bf16, self.state_bits = device, param_bf16, state_bits
+        self.sizes, self.shapes = sizes, [p.shape for p in params]
+        self.params, self.masters, self.exp_avg, self.exp_avg_sq, self.exp_avg_scale, self.exp_avg_sq_scale = lists
+        self._flat, self._ptrs, self._table = flat, [t.data_ptr() for t in flat], table
 
     def _rows(self, grads: Sequence[torch.Tensor]) -> np.ndarray:
         """The step's table; tensors that moved since the last one are checked again."""

@@ -1,0 +1,66 @@
+"""The AdamW handle's bookkeeping, without a GPU: tensors that say they are on one, and a library that writes
+down what it is given."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import async_rl_b200 as bi
+from async_rl_b200 import optim
+
+
+class Fake(torch.Tensor):
+    """A CPU tensor that passes for the device's."""
+    is_cuda = property(lambda self: True)
+
+    def get_device(self):
+        return self.device.index
+
+
+def fake(*shape, dtype=torch.float32):
+    return torch.zeros(*shape, dtype=dtype).as_subclass(Fake)
+
+
+class Library:
+    def __init__(self):
+        self.tables = []
+
+    def bi_adamw_step(self, table, n, cfg, grad_scale, step_dev, status, stream):
+        rows = (ctypes.c_int64 * (8 * n)).from_address(table)
+        self.tables.append(np.array(rows).reshape(n, 8))
+        return 0
+
+
+@pytest.fixture
+def lib(monkeypatch):
+    got = Library()
+    monkeypatch.setattr(optim._lib, "load", lambda: got)
+    monkeypatch.setattr(optim, "_stream", lambda dev: 0)
+    return got
+
+
+def handle(*shapes, dtype=torch.float32):
+    p, m, v = ([fake(*s, dtype=d) for s in shapes] for d in (dtype, torch.float32, torch.float32))
+    return bi.AdamWState(p, None, m, v)
+
+
+def step(st, grads, lib):
+    bi.adamw_step(st, grads, 1, 1e-3)
+    return lib.tables[-1]
+
+
+@pytest.mark.parametrize("other", [lambda: fake(299), lambda: fake(300, dtype=torch.float64),
+                                   lambda: fake(20, 15).t(), lambda: fake(300, dtype=torch.bfloat16)])
+def test_a_refused_binding_leaves_the_handle_as_it_was(other, lib):
+    """The storage is replaced by one that is refused, and put back: the next step is the first one's again."""
+    st = handle((300,), (40, 3))
+    g = [fake(300), fake(40, 3)]
+    first = step(st, g, lib)
+    old = st.params[0].data
+    st.params[0].data = other()
+    with pytest.raises(ValueError):
+        step(st, g, lib)
+    st.params[0].data = old
+    assert st.sizes == [300, 120] and st.shapes == [(300,), (40, 3)] and not st.param_bf16 and st.state_bits == 32
+    assert np.array_equal(step(st, g, lib), first)
