@@ -86,11 +86,14 @@ class AdamWState:
         self.params, self.masters, self.exp_avg, self.exp_avg_sq, self.exp_avg_scale, self.exp_avg_sq_scale = lists
         self._flat, self._ptrs, self._table = flat, [t.data_ptr() for t in flat], table
 
-    def _rows(self, grads: Sequence[torch.Tensor]) -> np.ndarray:
-        """The step's table; tensors that moved since the last one are checked again."""
+    def _follow(self):
+        """Tensors that moved since the last step are checked again."""
         if list(map(torch.Tensor.data_ptr, self._flat)) != self._ptrs:
             self._bind(self.params, self.masters, self.exp_avg, self.exp_avg_sq, self.exp_avg_scale,
                        self.exp_avg_sq_scale)
+
+    def _rows(self, grads: Sequence[torch.Tensor]) -> np.ndarray:
+        """The step's table."""
         self._table[:, 2] = list(map(torch.Tensor.data_ptr, grads))
         return self._table
 
@@ -119,6 +122,7 @@ def adamw_step(state: AdamWState, grads: Sequence[torch.Tensor], step: Union[int
     contiguous float32 or bfloat16 tensor (all of one type) for each param, of its shape.  ``step`` counts
     from 1; as a CUDA int64 tensor it is read when the kernel runs, so that a captured step can be
     replayed.  ``grad_scale``: a CUDA float32 scalar that multiplies the gradients.  Returns status."""
+    state._follow()  # before the gradients are held to the tensors' shapes
     dev = state.device
     n = len(state.params)
     if len(grads) != n:

@@ -64,3 +64,14 @@ def test_a_refused_binding_leaves_the_handle_as_it_was(other, lib):
     st.params[0].data = old
     assert st.sizes == [300, 120] and st.shapes == [(300,), (40, 3)] and not st.param_bf16 and st.state_bits == 32
     assert np.array_equal(step(st, g, lib), first)
+
+
+def test_gradients_are_held_to_the_tensors_of_this_step(lib):
+    """Every tensor replaced by a larger one: gradients of the old size would be read past their end."""
+    st = handle((300,))
+    step(st, [fake(300)], lib)
+    for t in st.tensors():
+        t.data = fake(5000)
+    with pytest.raises(ValueError, match="shape"):
+        step(st, [fake(300)], lib)
+    assert step(st, [fake(5000)], lib)[0, 7] == 5000
