@@ -2,6 +2,7 @@
 from __future__ import annotations
 
 import ctypes
+import operator
 from typing import List, Optional, Sequence, Union
 
 import numpy as np
@@ -11,6 +12,7 @@ from . import _lib
 from .api import _ptr, _raise_host, _stream
 from .attention import _on, _status
 
+_nbytes, _shape, _dtype = (operator.attrgetter(a) for a in ("nbytes", "shape", "dtype"))
 STATE_BLOCK = 256  # elements that share a scale in the 8-bit states
 
 
@@ -34,8 +36,9 @@ class AdamWState:
     ``params``: float32 or bfloat16, all of one type.  ``masters``: float32 weights of bfloat16 params
     (the update is made there and rounded into the param), or None.  ``exp_avg``, ``exp_avg_sq``:
     float32, or float8_e4m3fn with ``exp_avg_scale`` and ``exp_avg_sq_scale`` (float32, one for each
-    256 elements): then m = exp_avg * scale and sqrt(v) = exp_avg_sq * scale.  A tensor whose storage is
-    replaced (``param.data = ...``) is checked anew at the next step."""
+    256 elements): then m = exp_avg * scale and sqrt(v) = exp_avg_sq * scale.  A tensor that is replaced
+    (``param.data = ...``) is checked anew at the next step: a param of another address, shape, type or layout,
+    a state of another address or size in bytes."""
 
     def __init__(self, params: Sequence[torch.Tensor], masters: Optional[Sequence[torch.Tensor]],
                  exp_avg: Sequence[torch.Tensor], exp_avg_sq: Sequence[torch.Tensor],
@@ -85,10 +88,17 @@ class AdamWState:
         self.sizes, self.shapes = sizes, [p.shape for p in params]
         self.params, self.masters, self.exp_avg, self.exp_avg_sq, self.exp_avg_scale, self.exp_avg_sq_scale = lists
         self._flat, self._ptrs, self._table = flat, [t.data_ptr() for t in flat], table
+        self._nbytes, self._dtypes = [t.nbytes for t in flat], [p.dtype for p in params]
 
     def _follow(self):
-        """Tensors that moved since the last step are checked again."""
-        if list(map(torch.Tensor.data_ptr, self._flat)) != self._ptrs:
+        """Tensors that are not what they were at the last step are checked again."""
+        # All addresses and sizes in bytes, and what else a gradient is held to.  (57 parameters with masters and 32-bit
+        # states: 40 us of this call's 70; types and layouts of the states as well would be 20 more, and a state seen
+        # as another type or order of the same bytes is still the same memory.)
+        params = self.params
+        if (list(map(torch.Tensor.data_ptr, self._flat)) != self._ptrs or list(map(_nbytes, self._flat)) != self._nbytes or
+                list(map(_shape, params)) != self.shapes or list(map(_dtype, params)) != self._dtypes or
+                not all(map(torch.Tensor.is_contiguous, params))):
             self._bind(self.params, self.masters, self.exp_avg, self.exp_avg_sq, self.exp_avg_scale,
                        self.exp_avg_sq_scale)
 

@@ -75,3 +75,37 @@ def test_gradients_are_held_to_the_tensors_of_this_step(lib):
     with pytest.raises(ValueError, match="shape"):
         step(st, [fake(300)], lib)
     assert step(st, [fake(5000)], lib)[0, 7] == 5000
+
+
+HALF, EVERY_OTHER = (lambda t: t[:100]), (lambda t: t[::2])
+
+
+@pytest.mark.parametrize("other,which", [(HALF, 0), (HALF, 1), (HALF, 2), (EVERY_OTHER, 0), (EVERY_OTHER, 1),
+                                         (lambda t: t.view(torch.int32), 0), (lambda t: t.view(20, 15).t(), 0)])
+def test_another_size_type_or_layout_at_the_same_address_is_refused(other, which, lib):
+    """Of a param, exp_avg or exp_avg_sq."""
+    st = handle((300,), (40, 3))
+    g = [fake(300), fake(40, 3)]
+    step(st, g, lib)
+    t = st.tensors()[2 * which]
+    old = t.data
+    t.data = other(old)
+    assert t.data_ptr() == old.data_ptr()
+    n = len(lib.tables)
+    for _ in range(2):
+        with pytest.raises(ValueError):
+            step(st, g, lib)
+    assert len(lib.tables) == n
+    t.data = old
+    step(st, g, lib)
+
+
+def test_all_tensors_shrunk_or_reshaped_in_place_are_followed(lib):
+    st = handle((300,), (40, 3))
+    step(st, [fake(300), fake(40, 3)], lib)
+    for t in st.tensors()[::2]:
+        t.data = t.data[:100]
+    st.params[1].data = st.params[1].data.view(3, 40)
+    with pytest.raises(ValueError, match="shape"):
+        step(st, [fake(300), fake(40, 3)], lib)
+    assert step(st, [fake(100), fake(3, 40)], lib)[:, 7].tolist() == [100, 120]
