@@ -88,6 +88,9 @@ class AdamWState:
         self.sizes, self.shapes = sizes, [p.shape for p in params]
         self.params, self.masters, self.exp_avg, self.exp_avg_sq, self.exp_avg_scale, self.exp_avg_sq_scale = lists
         self._flat, self._ptrs, self._table = flat, [t.data_ptr() for t in flat], table
+        # what the step writes, in order of addresses
+        self._starts, self._ends = (np.array(x, dtype=np.int64) for x in (zip(*spans) if spans else ((0,), (0,))))
+        self._grads = None  # addresses and element size that were held against them
         self._nbytes, self._dtypes = [t.nbytes for t in flat], [p.dtype for p in params]
 
     def _follow(self):
@@ -102,9 +105,16 @@ class AdamWState:
             self._bind(self.params, self.masters, self.exp_avg, self.exp_avg_sq, self.exp_avg_scale,
                        self.exp_avg_sq_scale)
 
-    def _rows(self, grads: Sequence[torch.Tensor]) -> np.ndarray:
+    def _rows(self, grads: Sequence[torch.Tensor], itemsize: int) -> np.ndarray:
         """The step's table."""
-        self._table[:, 2] = list(map(torch.Tensor.data_ptr, grads))
+        ptrs = list(map(torch.Tensor.data_ptr, grads))
+        self._table[:, 2] = ptrs
+        if self._grads != (ptrs, itemsize):  # a matter of the addresses alone
+            low, sizes = self._table[:, 2], self._table[:, 7]
+            before = np.searchsorted(self._starts, low + sizes * itemsize) - 1  # the last that starts before the end
+            if np.any((sizes > 0) & (before >= 0) & (self._ends[before] > low)):
+                raise ValueError("a gradient may not overlap a tensor that the step writes")
+            self._grads = ptrs, itemsize
         return self._table
 
     @staticmethod
@@ -157,7 +167,7 @@ def adamw_step(state: AdamWState, grads: Sequence[torch.Tensor], step: Union[int
                                    grad_scale.dtype != torch.float32 or grad_scale.numel() != 1):
         raise ValueError(f"grad_scale must be a CUDA float32 tensor of one element on {dev}")
     st = _status(status, dev)
-    table = state._rows(grads)
+    table = state._rows(grads, 4 if gt is torch.float32 else 2)
     cfg = _lib.AdamWCfg(float(lr), float(beta1), float(beta2), float(eps), float(weight_decay), int(step),
                         state.state_bits, int(state.param_bf16), int(gt == torch.bfloat16), 0)
     with _on(dev):

@@ -60,7 +60,7 @@ typedef struct bi_adamw_cfg {
  *               replayed for other steps), or NULL.  A t below 1 raises BI_ERR_INVALID_ARG in
  *               *dev_status and leaves the tensors as they were.
  * count = 0 and tensors of no elements are fine.  All tensors have a master or none has; a master
- * needs param_bf16 = 1.  Tensors of one call may not overlap.
+ * needs param_bf16 = 1.  Tensors of one call may not overlap (gradients may overlap each other).
  * Returns BI_ERR_INVALID_ARG for a NULL or misaligned pointer, masters given for some tensors only,
  * a step below 1, lr, eps or weight_decay below 0 or not finite, or a beta outside [0, 1).
  */

@@ -109,3 +109,26 @@ def test_all_tensors_shrunk_or_reshaped_in_place_are_followed(lib):
     with pytest.raises(ValueError, match="shape"):
         step(st, [fake(300), fake(40, 3)], lib)
     assert step(st, [fake(100), fake(3, 40)], lib)[:, 7].tolist() == [100, 120]
+
+
+@pytest.mark.parametrize("grads", [
+    lambda st, flat: [st.params[0], fake(40, 3)], lambda st, flat: [fake(300), st.exp_avg_sq[1]],
+    lambda st, flat: [flat[10:310], fake(40, 3)], lambda st, flat: [fake(300), flat[299:419].view(40, 3)]])
+def test_gradients_may_not_overlap_what_the_step_writes(grads, lib):
+    """A gradient that is written while other threads still read it gives results that depend on timing."""
+    flat = fake(900)
+    p = [flat[:300], flat[500:620].view(40, 3)]
+    st = bi.AdamWState(p, None, [fake(300), fake(40, 3)], [fake(300), fake(40, 3)])
+    good = [flat[620:720].expand(3, 100).reshape(300), flat[300:420].view(40, 3)]
+    for _ in range(2):
+        step(st, good, lib)
+        n = len(lib.tables)
+        with pytest.raises(ValueError, match="overlap"):
+            step(st, grads(st, flat), lib)
+        assert len(lib.tables) == n
+
+
+def test_gradients_may_share_memory_and_be_empty(lib):
+    st = handle((300,), (0,), (300,))
+    g = fake(400)
+    assert step(st, [g[:300], g[:0], g[100:]], lib)[:, 7].tolist() == [300, 0, 300]
