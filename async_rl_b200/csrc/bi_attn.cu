@@ -200,11 +200,16 @@ bi_status bi_attn_fwd(const uint16_t* q, const uint16_t* k, const uint16_t* v, i
   if (!dev_status || !sizes_ok(z) || !(scale > 0.f) || !std::isfinite(scale)) return BI_ERR_INVALID_ARG;
   if (!shape_ok(z)) return BI_ERR_UNSUPPORTED_SHAPE;
   if (S > 0 && (!q_offsets || !k_offsets)) return BI_ERR_INVALID_ARG;
-  if (Tq > 0 && (!rows_ok(q, q_ld, Hq, D) || !out || !aligned16(out) || !lse || out == q || out == k || out == v))
+  if (Tq > 0 && (!rows_ok(q, q_ld, Hq, D) || !out || !aligned16(out) || !lse))
     return BI_ERR_INVALID_ARG;
   if (Tk > 0 && (!rows_ok(k, k_ld, Hkv, D) || !rows_ok(v, v_ld, Hkv, D))) return BI_ERR_INVALID_ARG;
   const FwdLayout L = fwd_layout(z);
   if (!ws || ws_bytes < L.total || (reinterpret_cast<uintptr_t>(ws) & 255u)) return BI_ERR_WORKSPACE;
+  if (aliased({span_rows(out, Tq, static_cast<int64_t>(Hq) * D, Hq, D), span(lse, static_cast<uint64_t>(Hq) * Tq * 4),
+               span(dev_status, 4), span(ws, L.total)},
+              {span_rows(q, Tq, q_ld, Hq, D), span_rows(k, Tk, k_ld, Hkv, D), span_rows(v, Tk, v_ld, Hkv, D),
+               span(q_offsets, (S + int64_t{1}) * 8), span(k_offsets, (S + int64_t{1}) * 8), span(k_lens, S * int64_t{4})}))
+    return BI_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (S == 0 || Tq == 0) return cudaMemsetAsync(dev_status, 0, sizeof(int32_t), s) == cudaSuccess ? BI_OK : BI_ERR_CUDA;
   const int sms = attn_device();
@@ -289,13 +294,20 @@ bi_status bi_attn_bwd(const uint16_t* dout, int64_t dout_ld, const uint16_t* q, 
   if (!shape_ok(z)) return BI_ERR_UNSUPPORTED_SHAPE;
   if (S > 0 && (!q_offsets || !k_offsets)) return BI_ERR_INVALID_ARG;
   if (Tq > 0 && (!rows_ok(q, q_ld, Hq, D) || !rows_ok(dout, dout_ld, Hq, D) || !rows_ok(dq, dq_ld, Hq, D) || !out ||
-                 !aligned16(out) || !lse || dq == q || dq == dout || dq == out))
+                 !aligned16(out) || !lse))
     return BI_ERR_INVALID_ARG;
   if (Tk > 0 && (!rows_ok(k, k_ld, Hkv, D) || !rows_ok(v, v_ld, Hkv, D) || !rows_ok(dk, dk_ld, Hkv, D) ||
-                 !rows_ok(dv, dv_ld, Hkv, D) || dk == k || dk == v || dv == k || dv == v || dk == dv || dk == dq || dv == dq))
+                 !rows_ok(dv, dv_ld, Hkv, D)))
     return BI_ERR_INVALID_ARG;
   const BwdLayout L = bwd_layout(z);
   if (!ws || ws_bytes < L.total || (reinterpret_cast<uintptr_t>(ws) & 255u)) return BI_ERR_WORKSPACE;
+  if (aliased({span_rows(dq, Tq, dq_ld, Hq, D), span_rows(dk, Tk, dk_ld, Hkv, D), span_rows(dv, Tk, dv_ld, Hkv, D),
+               span(dev_status, 4), span(ws, L.total)},
+              {span_rows(dout, Tq, dout_ld, Hq, D), span_rows(q, Tq, q_ld, Hq, D), span_rows(k, Tk, k_ld, Hkv, D),
+               span_rows(v, Tk, v_ld, Hkv, D), span_rows(out, Tq, static_cast<int64_t>(Hq) * D, Hq, D),
+               span(lse, static_cast<uint64_t>(Hq) * Tq * 4), span(q_offsets, (S + int64_t{1}) * 8),
+               span(k_offsets, (S + int64_t{1}) * 8), span(k_lens, S * int64_t{4})}))
+    return BI_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (S == 0 || (Tq == 0 && Tk == 0))
     return cudaMemsetAsync(dev_status, 0, sizeof(int32_t), s) == cudaSuccess ? BI_OK : BI_ERR_CUDA;

@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <initializer_list>
 #include <mutex>
 #include <vector>
 
@@ -95,6 +96,51 @@ inline EncodeTiledFn encode_fn() {
   return fn;
 }
 
+
+// What a call reads or writes: `rows` rows of `row` bytes, `ld` bytes apart (1 row: a plain array).
+struct Span {
+  uintptr_t at;
+  uint64_t rows, row, ld;
+};
+inline Span span(const void* p, uint64_t bytes) {
+  return Span{reinterpret_cast<uintptr_t>(p), p && bytes ? 1u : 0u, bytes, bytes};
+}
+// bf16 rows of `heads` heads, as the attention layer's tensors are
+inline Span span_rows(const void* p, int64_t rows, int64_t ld, int64_t heads, int64_t D) {
+  return Span{reinterpret_cast<uintptr_t>(p), p ? static_cast<uint64_t>(rows) : 0u, static_cast<uint64_t>(heads * D * 2),
+              static_cast<uint64_t>(ld * 2)};
+}
+// Whether two of them share a byte.  Slices of one buffer have one stride: their rows keep their distance.  With
+// two strides each row of one is held against the other's rows around it.
+inline bool overlap(const Span& a, const Span& b) {
+  if (a.rows == 0 || b.rows == 0) return false;
+  const uintptr_t ae = a.at + (a.rows - 1) * a.ld + a.row, be = b.at + (b.rows - 1) * b.ld + b.row;
+  if (ae <= b.at || be <= a.at) return false;
+  if (a.rows == 1 && b.rows == 1) return true;
+  const Span &few = a.rows < b.rows ? a : b, &many = a.rows < b.rows ? b : a;
+  // rows of `few` that reach into the range of `many`
+  const uintptr_t ms = many.at, me = many.at + (many.rows - 1) * many.ld + many.row;
+  uint64_t i = few.at + few.row <= ms && few.rows > 1 ? (ms - few.at - few.row) / few.ld + 1 : 0;
+  for (uint64_t n = 0; i < few.rows && few.at + i * few.ld < me; ++i, ++n) {
+    const uintptr_t lo = few.at + i * few.ld, hi = lo + few.row;
+    if (hi <= ms) continue;
+    // the first row of `many` that ends behind lo
+    const uint64_t j = lo < ms + many.row ? 0 : (lo - ms - many.row) / many.ld + 1;
+    if (j < many.rows && ms + j * many.ld < hi) return true;
+    if (few.ld == many.ld && n > 0) return false;  // inside both, every row is like this one
+  }
+  return false;
+}
+// Outputs may share memory with no input and with no other output.
+inline bool aliased(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+  for (const Span* o = outs.begin(); o != outs.end(); ++o) {
+    for (const Span* p = outs.begin(); p != o; ++p)
+      if (overlap(*o, *p)) return true;
+    for (const Span& i : ins)
+      if (overlap(*o, i)) return true;
+  }
+  return false;
+}
 
 // SMs of the current device (0 where that cannot be read), asked once per device.
 inline int sm_count() {
