@@ -62,7 +62,11 @@ bi_status bi_qk_norm_rope(const uint16_t* q, const uint16_t* k, int64_t q_ld, in
   if (T > 0 && (!positions || !rows_ok(q, q_ld, Hq, D) || !rows_ok(k, k_ld, Hkv, D) || !rows_ok(q_out, q_out_ld, Hq, D) ||
                 !rows_ok(k_out, k_out_ld, Hkv, D)))
     return BI_ERR_INVALID_ARG;
-  if (T > 0 && (q == q_out || k == k_out || q_out == k_out)) return BI_ERR_INVALID_ARG;
+  const uint64_t gain_bytes = static_cast<uint64_t>(D) * 2;
+  if (aliased({span_rows(q_out, T, q_out_ld, Hq, D), span_rows(k_out, T, k_out_ld, Hkv, D), span(dev_status, 4)},
+              {span_rows(q, T, q_ld, Hq, D), span_rows(k, T, k_ld, Hkv, D), span(gq, gain_bytes), span(gk, gain_bytes),
+               span(positions, T * 4), span(inv_freq, R * uint64_t{2})}))
+    return BI_ERR_INVALID_ARG;
   const int sms = sm_count();
   if (sms <= 0) return BI_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -117,9 +121,17 @@ bi_status bi_qk_norm_rope_bwd(const uint16_t* dq_out, const uint16_t* dk_out, in
                 !rows_ok(dq, dq_ld, Hq, D) || !rows_ok(dk, dk_ld, Hkv, D)))
     return BI_ERR_INVALID_ARG;
   if (T > 0 && gq && (!rows_ok(q, q_ld, Hq, D) || !rows_ok(k, k_ld, Hkv, D))) return BI_ERR_INVALID_ARG;
-  if (T > 0 && (dq == dq_out || dk == dk_out || dq == q || dk == k || dq == dk)) return BI_ERR_INVALID_ARG;
+  if (T > 0 && !gq && (dq == q || dk == k)) return BI_ERR_INVALID_ARG;  // not read, their strides may say nothing
   if (gq && (!ws || ws_bytes < bi_qk_norm_rope_bwd_workspace_bytes(D) || (reinterpret_cast<uintptr_t>(ws) & 255u)))
     return BI_ERR_WORKSPACE;
+  const uint64_t gain_bytes = static_cast<uint64_t>(D) * 2, gain_grad = gq ? 2 * gain_bytes : 0;
+  const int64_t read = gq ? T : 0;  // rows of q and k
+  if (aliased({span_rows(dq, T, dq_ld, Hq, D), span_rows(dk, T, dk_ld, Hkv, D), span(dgq, gain_grad), span(dgk, gain_grad),
+               span(dev_status, 4), span(ws, gq ? bi_qk_norm_rope_bwd_workspace_bytes(D) : 0)},
+              {span_rows(dq_out, T, dq_out_ld, Hq, D), span_rows(dk_out, T, dk_out_ld, Hkv, D),
+               span_rows(q, read, q_ld, Hq, D), span_rows(k, read, k_ld, Hkv, D), span(gq, gain_bytes),
+               span(gk, gain_bytes), span(positions, T * 4), span(inv_freq, R * uint64_t{2})}))
+    return BI_ERR_INVALID_ARG;
   const int sms = sm_count();
   if (sms <= 0 || sms > kMaxSms) return BI_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -9,7 +9,7 @@ import pytest
 
 from async_rl_b200 import _lib
 from async_rl_b200.build import build
-from tests.test_layer_refusals_cpu import ARG, BWD, FWD, _call
+from tests.test_layer_refusals_cpu import ARG, BWD, FWD, QK, QKB, _call
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
@@ -39,6 +39,22 @@ def test_attn_fwd(lib, out, other):
 def test_attn_bwd(lib, out, other):
     base = {**BWD, **BWD_SAME, "kl": 200 << 20}
     assert _call(lib.bi_attn_bwd, base, **{out: base[other]}) == ARG
+
+
+QK_SAME = dict(Hq=4, Hkv=4, q_ld=1024, k_ld=1024)
+
+
+@pytest.mark.parametrize("out,other", pairs(["qo", "ko", "st"], ["q", "k", "gq", "gk", "pos", "inv"]))
+def test_qk_norm_rope(lib, out, other):
+    base = {**QK, **QK_SAME, "qo_ld": 1024, "ko_ld": 1024}
+    assert _call(lib.bi_qk_norm_rope, base, **{out: base[other]}) == ARG
+
+
+@pytest.mark.parametrize("out,other", pairs(["dq", "dk", "dgq", "dgk", "st", "ws"],
+                                            ["dqo", "dko", "q", "k", "gq", "gk", "pos", "inv"]))
+def test_qk_norm_rope_bwd(lib, out, other):
+    base = {**QKB, **QK_SAME, "dqo_ld": 1024, "dko_ld": 1024, "dq_ld": 1024, "dk_ld": 1024}
+    assert _call(lib.bi_qk_norm_rope_bwd, base, **{out: base[other]}) == ARG
 
 
 @pytest.mark.parametrize("shift", [512, 1024 + 16, 62 * 2048 + 1024 + 16, -512, -(63 * 2048 + 1024) + 16])
