@@ -13,7 +13,8 @@ EXPORTED = ("bi_workspace_bytes", "bi_workspace_bytes_min", "bi_workspace_bytes_
             "bi_status_string", "bi_version", "bi_debug_force_timeout_once", "bi_profile_enable",
             "bi_profile_reset", "bi_profile_read", "bi_gemm_bf16", "bi_rmsnorm", "bi_qk_norm_rope",
             "bi_qk_norm_rope_bwd_workspace_bytes", "bi_qk_norm_rope_bwd", "bi_adamw_step",
-            "bi_attn_fwd_workspace_bytes", "bi_attn_fwd", "bi_attn_bwd_workspace_bytes", "bi_attn_bwd")
+            "bi_attn_fwd_workspace_bytes", "bi_attn_fwd", "bi_attn_bwd_workspace_bytes", "bi_attn_bwd",
+            "bi_debug_attn_wait_limit_once")
 
 STATUS_NAMES = {0: "BI_OK", 1: "BI_ERR_INVALID_ARG", 2: "BI_ERR_UNSUPPORTED_SHAPE", 3: "BI_ERR_WORKSPACE",
                 4: "BI_ERR_CUDA", 5: "BI_ERR_TIMEOUT", 6: "BI_ERR_BAD_TARGET", 7: "BI_ERR_NONFINITE",
@@ -108,6 +109,8 @@ def load() -> ctypes.CDLL:
     lib.bi_attn_bwd.argtypes = [_p, _i64, _p, _p, _p, _i64, _i64, _i64, _p, _p, _p, _p, _p, _i32, _i64, _i64, _i32,
                                 _i32, _i32, _i32, f32, _p, _p, _p, _i64, _i64, _i64, _p, _p, _sz, _p]
     lib.bi_attn_bwd.restype = ctypes.c_int
+    lib.bi_debug_attn_wait_limit_once.argtypes = [_u64]
+    lib.bi_debug_attn_wait_limit_once.restype = None
     lib.bi_adamw_step.argtypes = [_p, _i32, _p, _p, _p, _p, _p]
     lib.bi_adamw_step.restype = ctypes.c_int
     _lib = lib

@@ -287,6 +287,7 @@ struct AtFwdShared {
   uint64_t done;
   uint32_t tmem_base;
   volatile uint32_t abort_flag;
+  volatile uint32_t begun;  // units that the loading thread has begun
 };
 constexpr int kAtSharedBytes = static_cast<int>((sizeof(AtFwdShared) + 127) / 128 * 128);
 
@@ -342,6 +343,14 @@ __device__ __forceinline__ float2 at_ex2(int pair, float2 x) {
 // A warp's wait for what MMAs left in tensor memory or what another role wrote.
 __device__ __forceinline__ bool at_wait(uint64_t* bar, uint32_t parity, const WaitCtl& wc) {
   const bool ok = __all_sync(0xffffffffu, mbar_wait<false>(bar, parity, wc));
+  tc_fence_after();
+  return ok;
+}
+
+// The ragged warp's wait: it has nothing to do with most units, and its next one may be the CTA's last.
+__device__ __forceinline__ bool at_wait_behind(uint64_t* bar, uint32_t parity, const WaitCtl& wc,
+                                               const volatile uint32_t* begun) {
+  const bool ok = __all_sync(0xffffffffu, mbar_wait_behind(bar, parity, wc, begun));
   tc_fence_after();
   return ok;
 }
@@ -414,7 +423,7 @@ __device__ __forceinline__ void at_fwd_load(AtFwdShared& sh, const AttnFwdArgs& 
   tma_prefetch_desc(mv);
   const uint32_t ring = smem + kRows * T::tile_bytes;
   const uint32_t qbytes = static_cast<uint32_t>(a.tpt * a.G) * 128u * (D / 64);
-  uint32_t qph = 0, g = 0;
+  uint32_t qph = 0, g = 0, begun = 0;
   // tile `pos` of the ring (keys of tile g at 2 g, values at 2 g + 1), for pair `pair`
   auto load = [&](uint32_t pos, uint32_t pair, const CUtensorMap* m, int32_t h, int32_t row) {
     if (pos >= T::slots) {
@@ -433,6 +442,7 @@ __device__ __forceinline__ void at_fwd_load(AtFwdShared& sh, const AttnFwdArgs& 
     const AtUnit& x = walk.x;
     const int32_t j = x.jb + walk.i - 1;
     if (walk.i == 1) {
+      sh.begun = ++begun;
 #pragma unroll
       for (int X = 0; X < kRows; ++X) {
         if (x.je(X) <= x.jb) continue;
@@ -482,7 +492,7 @@ __device__ __forceinline__ void at_fwd_ragged(AtFwdShared& sh, const AttnFwdArgs
     g += tiles;
     if (!x.ragged(x.n - 1)) continue;
     const uint32_t b = g % kAtPairs;
-    if (!at_wait(&sh.z_ask[b], (used >> b) & 1u, wc) || !at_wait(&sh.full[b], g / kAtPairs & 1u, wc)) return;
+    if (!at_wait_behind(&sh.z_ask[b], (used >> b) & 1u, wc, &sh.begun) || !at_wait(&sh.full[b], g / kAtPairs & 1u, wc)) return;
     used ^= 1u << b;
     at_zero_rows<D>(smem_p + (kRows + (2 * g - 1) % T::slots) * T::tile_bytes, x.q.lk - (x.n - 1) * kAtTile);
     if ((threadIdx.x & 31) == 0) mbar_arrive(&sh.z_full[b]);
@@ -832,6 +842,7 @@ __global__ void __launch_bounds__(AtFwdTile<D, kRows>::threads, 3 - kRows)
     }
     mbar_init(&sh.done, 1);
     sh.abort_flag = 0u;
+    sh.begun = 0u;
     fence_mbar_init_cluster();
   }
   if (warp == T::soft + 1) {

@@ -121,6 +121,7 @@ struct AtBwdShared {
   uint64_t z_ask[2], z_full[2];    // a unit's ragged last tile (A and B ring): loading; has its zeros
   uint32_t tmem_base;
   volatile uint32_t abort_flag;
+  volatile uint32_t begun;  // units that the loading thread has begun
 };
 constexpr int kAtBwdSharedBytes = static_cast<int>((sizeof(AtBwdShared) + 127) / 128 * 128);
 
@@ -176,6 +177,7 @@ __device__ __forceinline__ uint32_t at_bwd_begin(AtBwdShared& sh) {
     mbar_init(&sh.acc_full, 1);
     mbar_init(&sh.done, 1);
     sh.abort_flag = 0u;
+    sh.begun = 0u;
     fence_mbar_init_cluster();
   }
   if (threadIdx.x / 32 == kAtBwdProbs + 1) {
@@ -298,7 +300,7 @@ __device__ __forceinline__ void at_dkv_load(AtBwdShared& sh, const AttnBwdArgs& 
   AtRing<kAtSlotsA> ra;
   AtRing<kAtSlotsB> rb;
   AtRing<2> rs;
-  uint32_t hph = 0;
+  uint32_t hph = 0, begun = 0;
   AtBwdWalk<AtKvUnit> walk(a, nu);
   AtStep f;
   auto held = [&](int w, const CUtensorMap* m) {
@@ -314,6 +316,7 @@ __device__ __forceinline__ void at_dkv_load(AtBwdShared& sh, const AttnBwdArgs& 
     const AtKvUnit& x = walk.x;
     const int32_t i = x.i0 + walk.i - 1;
     const int32_t row = static_cast<int32_t>(x.q.q0) + i * a.tpt;
+    if (f.first) sh.begun = ++begun;
     if (f.first && !held(0, mk)) return;
     if (!mbar_wait<false>(&sh.a_empty[ra.slot], ra.phase ^ 1u, wc)) return;
     mbar_arrive_expect_tx(&sh.a_full[ra.slot], bytes);
@@ -439,7 +442,7 @@ __device__ __forceinline__ void at_dkv_ragged(AtBwdShared& sh, const AttnBwdArgs
     ra.skip(x.i1 - 1 - x.i0);
     rb.skip(x.i1 - 1 - x.i0);
     if (x.ragged) {
-      if (!at_wait(&sh.z_ask[0], ph, wc) || !at_wait(&sh.a_full[ra.slot], ra.phase, wc)) return;
+      if (!at_wait_behind(&sh.z_ask[0], ph, wc, &sh.begun) || !at_wait(&sh.a_full[ra.slot], ra.phase, wc)) return;
       at_zero_rows<D>(smem_p + T::ring_a + ra.slot * T::tile_bytes, x.rows);
       if ((threadIdx.x & 31) == 0) mbar_arrive(&sh.z_full[0]);
       if (!at_wait(&sh.z_ask[1], ph, wc) || !at_wait(&sh.b_full[rb.slot], rb.phase, wc)) return;
@@ -630,7 +633,7 @@ __device__ __forceinline__ void at_dq_load(AtBwdShared& sh, const AttnBwdArgs& a
   const uint32_t bytes = static_cast<uint32_t>(a.tpt * a.G) * 128u * (D / 64);
   AtRing<kAtSlotsA> ra;
   AtRing<kAtSlotsB> rb;
-  uint32_t hph = 0;
+  uint32_t hph = 0, begun = 0;
   AtBwdWalk<AtQUnit> walk(a, nu);
   AtStep f;
   auto held = [&](int w, const CUtensorMap* m) {
@@ -645,6 +648,7 @@ __device__ __forceinline__ void at_dq_load(AtBwdShared& sh, const AttnBwdArgs& a
   while (walk.step(f)) {
     const AtQUnit& x = walk.x;
     const int32_t key = static_cast<int32_t>(x.q.k0) + (walk.i - 1) * kAtTile;
+    if (f.first) sh.begun = ++begun;
     if (f.first && !held(0, mq)) return;
     if (!mbar_wait<false>(&sh.a_empty[ra.slot], ra.phase ^ 1u, wc)) return;
     mbar_arrive_expect_tx(&sh.a_full[ra.slot], T::tile_bytes);
@@ -752,7 +756,7 @@ __device__ __forceinline__ void at_dq_ragged(AtBwdShared& sh, const AttnBwdArgs&
     if (x.n == 0) continue;
     ra.skip(x.n - 1);
     if (x.ragged) {
-      if (!at_wait(&sh.z_ask[0], ph, wc) || !at_wait(&sh.a_full[ra.slot], ra.phase, wc)) return;
+      if (!at_wait_behind(&sh.z_ask[0], ph, wc, &sh.begun) || !at_wait(&sh.a_full[ra.slot], ra.phase, wc)) return;
       at_zero_rows<D>(smem_p + T::ring_a + ra.slot * T::tile_bytes, x.rows);
       if ((threadIdx.x & 31) == 0) mbar_arrive(&sh.z_full[0]);
       ph ^= 1u;

@@ -159,6 +159,29 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, const 
   }
 }
 
+// The same for a role that passes over many of another's turns before its own: the clock starts anew whenever
+// *turns, which the other counts up, has moved.  Such waits are long: the clock is read at every turn of the loop.
+__device__ __forceinline__ bool mbar_wait_behind(uint64_t* bar, uint32_t parity, const WaitCtl& w,
+                                                 const volatile uint32_t* turns) {
+  if (mbar_test(bar, parity)) return true;
+  uint64_t t0 = globaltimer_ns();
+  uint32_t seen = *turns;
+  while (!mbar_test(bar, parity)) {
+    if (*w.abort_flag) return false;
+    const uint32_t now = *turns;
+    const uint64_t t = globaltimer_ns();
+    if (now != seen) {
+      seen = now;
+      t0 = t;
+    } else if (t - t0 > w.limit_ns) {
+      raise_status(w.status, 5 /* BI_ERR_TIMEOUT */);
+      *w.abort_flag = 1u;
+      return false;
+    }
+  }
+  return true;
+}
+
 // ----------------------------------------------------------------------------------------------
 // TMA (tensor tile loads, no cluster-wide delivery)
 // ----------------------------------------------------------------------------------------------

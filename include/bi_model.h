@@ -157,6 +157,11 @@ BI_API bi_status bi_attn_bwd(const uint16_t* dout, int64_t dout_ld, const uint16
                              int64_t dq_ld, int64_t dk_ld, int64_t dv_ld, int32_t* dev_status, void* ws,
                              size_t ws_bytes, void* stream);
 
+/* Test hook, not for production use: the next bi_attn_fwd or bi_attn_bwd on this host thread that launches
+ * kernels gives each of their waits this limit in nanoseconds, in place of 4 s and 40 ns a key and query row.
+ * 0 disables the hook. */
+BI_API void bi_debug_attn_wait_limit_once(uint64_t limit_ns);
+
 #ifdef __cplusplus
 }
 #endif
