@@ -291,8 +291,10 @@ struct AtFwdShared {
 };
 constexpr int kAtSharedBytes = static_cast<int>((sizeof(AtFwdShared) + 127) / 128 * 128);
 
+// The difference by itself, whatever it is taken of: contracted with a product in one kernel and not in another
+// it would give a row other bits in a prefill than in a decode step.
 __device__ __forceinline__ float attn_join_scale(float from, float to) {
-  return to == -INFINITY ? 0.f : ex2_approx(from - to);
+  return to == -INFINITY ? 0.f : ex2_approx(__fsub_rn(from, to));
 }
 
 // A CTA's r-th unit.  Units are listed dearest first; every other round runs backwards, so that a CTA
@@ -683,17 +685,17 @@ __device__ __forceinline__ void at_fwd_softmax(AtFwdShared& sh, const AttnFwdArg
             mx[b] = fmaxf(fmaxf(mx[b], __uint_as_float(s[b][e])), __uint_as_float(s[b][e + 1]));
           mx[b] = fmaxf(mx[b], __uint_as_float(s[b][31]));
         }
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.c;
+        const float top = __fmul_rn(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), a.c);  // rounded: see attn_join_scale
         if (first) {
           m = top;
         } else {
-          const bool raise = top > m + 8.f;
+          const bool raise = top > __fadd_rn(m, 8.f);
           if (__any_sync(0xffffffffu, raise)) {
             at_rare();
             // S of this tile was issued behind the last product into O: O is complete
             const float alpha = raise ? attn_join_scale(m, top) : 1.f;
             if (raise) m = top;
-            l *= alpha;
+            l = __fmul_rn(l, alpha);
 #pragma unroll 1
             for (int b = 0; b < D / 16; ++b) {
               uint32_t o[16];
@@ -755,7 +757,7 @@ __device__ __forceinline__ void at_fwd_softmax(AtFwdShared& sh, const AttnFwdArg
       }
       const float m_new = fmaxf(m_run, m);
       const float ka = fresh ? 0.f : attn_join_scale(m_run, m_new), kb = fresh ? 1.f : attn_join_scale(m, m_new);
-      l_run = fresh ? l : fmaf(l, kb, l_run * ka);
+      l_run = fresh ? l : fmaf(l, kb, __fmul_rn(l_run, ka));
       m_run = m_new;
       const float inv = l_run > 0.f || l_run != l_run ? 1.f / l_run : 0.f;
       if (fresh && last) {  // a row of one chunk: all of O at once
@@ -920,7 +922,7 @@ __global__ void __launch_bounds__(kAtJoinThreads)
       const float2 ml = a.part_ml[pr];
       const float m_new = fmaxf(m_run, ml.x);
       const float ka = c == 0 ? 0.f : attn_join_scale(m_run, m_new), kb = c == 0 ? 1.f : attn_join_scale(ml.x, m_new);
-      l_run = c == 0 ? ml.y : fmaf(ml.y, kb, l_run * ka);
+      l_run = c == 0 ? ml.y : fmaf(ml.y, kb, __fmul_rn(l_run, ka));
       m_run = m_new;
 #pragma unroll
       for (int e = 0; e < N; ++e) {
