@@ -22,6 +22,7 @@ constexpr int kAdamUnit = 256;                      // elements of a warp's turn
 constexpr int kAdamChunk = kAdamUnit * (kAdamThreads / 32);  // elements of a block
 constexpr float kE4m3Max = 448.0f;
 constexpr float kE4m3Inv = 1.0f / 448.0f;
+constexpr float kF32Max = 3.4028235e38f;
 constexpr float kE4m3Tiny = 0.001953125f;           // 2^-9, the smallest positive value
 
 struct AdamHyper {
@@ -233,8 +234,10 @@ __global__ void __launch_bounds__(kAdamThreads, kState8 ? 6 : 3) k_adamw(const _
         }
       mm = adam_warp_max(mm);
       mv = adam_warp_max(mv);
-      // a subnormal maximum's reciprocal would be infinite; sqrt(v) is never that small
-      const float im = mm > 0.f ? fminf(__fmul_rn(__frcp_rn(mm), kE4m3Max), 3.4028235e38f) : 0.f;
+      // 448 / max is infinite for a maximum below 1.3e-36: zeros then, which a step with any eps to speak of would
+      // not tell from it; sqrt(v) is never that small
+      float im = __fmul_rn(__frcp_rn(mm), kE4m3Max);
+      if (im > kF32Max) im = mm = 0.f;
       const float iv = mv > 0.f ? __fmul_rn(__frcp_rn(mv), kE4m3Max) : 0.f;
       uint32_t mw[2] = {}, vw[2] = {};
 #pragma unroll

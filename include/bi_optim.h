@@ -40,9 +40,10 @@ typedef struct bi_adamw_tensor {
 /*
  * 8-bit states: a block of 256 consecutive elements (the last one may be short) holds x as
  * code * scale with scale = max|x| * fl(1 / 448) (448 = the largest e4m3 value) and the code
- * x * (448 * fl(1 / max|x|)) rounded to nearest even; x is m for exp_avg and sqrt(v) for exp_avg_sq, whose root halves the range of
- * exponents.  A sqrt(v) above zero never becomes the code of zero (it takes the smallest one, 2^-9):
- * a zero there would turn a small gradient into an unbounded update.
+ * x * (448 * fl(1 / max|x|)) rounded to nearest even; x is m for exp_avg and sqrt(v) for exp_avg_sq, whose
+ * root halves the range of exponents.  Where 448 * fl(1 / max|x|) is not finite (a maximum below 1.3e-36)
+ * the block is held as zeros with scale 0.  A sqrt(v) above zero never becomes the code of zero (it takes the
+ * smallest one, 2^-9): a zero there would turn a small gradient into an unbounded update.
  */
 typedef struct bi_adamw_cfg {
   double lr, beta1, beta2, eps, weight_decay;
