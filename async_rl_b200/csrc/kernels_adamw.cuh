@@ -227,11 +227,16 @@ __global__ void __launch_bounds__(kAdamThreads, kState8 ? 6 : 3) k_adamw(const _
     if (kState8) {
       float mm = 0.f, mv = 0.f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
+      for (int e = 0; e < 8; ++e) {
+        // an infinity as the block's maximum would make NaN of all its elements: it becomes one itself (fmaxf
+        // passes NaN over)
+        x.m.x[e] = fabsf(x.m.x[e]) <= kF32Max ? x.m.x[e] : __int_as_float(0x7fffffff);
+        root[e] = root[e] <= kF32Max ? root[e] : __int_as_float(0x7fffffff);
         if (i0 + e < n) {
           mm = fmaxf(mm, fabsf(x.m.x[e]));
           mv = fmaxf(mv, root[e]);
         }
+      }
       mm = adam_warp_max(mm);
       mv = adam_warp_max(mv);
       // 448 / max is infinite for a maximum below 1.3e-36: zeros then, which a step with any eps to speak of would

@@ -43,7 +43,9 @@ typedef struct bi_adamw_tensor {
  * x * (448 * fl(1 / max|x|)) rounded to nearest even; x is m for exp_avg and sqrt(v) for exp_avg_sq, whose
  * root halves the range of exponents.  Where 448 * fl(1 / max|x|) is not finite (a maximum below 1.3e-36)
  * the block is held as zeros with scale 0.  A sqrt(v) above zero never becomes the code of zero (it takes the
- * smallest one, 2^-9): a zero there would turn a small gradient into an unbounded update.
+ * smallest one, 2^-9): a zero there would turn a small gradient into an unbounded update.  max is taken of the
+ * finite elements; one that is not finite is held as NaN, and the other elements of its block are what they would
+ * be without it.
  */
 typedef struct bi_adamw_cfg {
   double lr, beta1, beta2, eps, weight_decay;

@@ -76,3 +76,30 @@ def test_a_block_without_gradients_decays_to_zero(cuda_device):
             else:
                 assert torch.equal(codes, first), t
     assert float(scale) == 0
+
+
+@pytest.mark.parametrize("bad", [float("inf"), -float("inf"), float("nan"), 1e25])
+def test_elements_that_are_not_finite_stay_their_own(bad, cuda_device):
+    """One gradient of a block is infinite, NaN or has an infinite square: the block's other elements have the
+    bits of a block whose element has no gradient, in that step and in later ones.  (1e25 is a finite m and the
+    block's maximum, before which the others vanish; they stay finite.)"""
+    gen = torch.Generator().manual_seed(2)
+    n, at = 600, [5, 300]
+    grads = [torch.randn(n, generator=gen) * 1e-3 for _ in range(4)]
+    w = torch.randn(n, generator=gen)
+    runs = []
+    for worst in (0.0, bad):
+        st = bi.AdamWState.allocate([w.clone().to(cuda_device)], state_bits=8)
+        for t, g in enumerate(grads, 1):
+            g = g.clone()
+            g[at] = worst if t == 2 else 0.0
+            bi.check_status(bi.adamw_step(st, [g.to(cuda_device)], t, **HYPER))
+        runs.append([st.params[0].cpu(), st.exp_avg[0].cpu().float(), st.exp_avg_sq[0].cpu().float(),
+                     st.exp_avg_scale[0].cpu(), st.exp_avg_sq_scale[0].cpu()])
+    keep = torch.ones(n, dtype=torch.bool)
+    keep[at] = False
+    for a, b in zip(*runs):
+        k = keep if a.numel() == n else slice(None)
+        assert torch.isfinite(b[k]).all()
+        assert bad == 1e25 or torch.equal(a[k], b[k])
+    assert torch.isnan(runs[1][2][at]).all()
