@@ -48,13 +48,15 @@ bool launch(const bi_adamw_tensor* ts, int32_t& at, int32_t count, const bi_adam
   tab->count = n;
   const unsigned grid = static_cast<unsigned>(blocks);
   ProfScope ps(kKAdamW, s);
-#define BI_ADAM(S8, PB, MA, GB)                                                                     \
-  if ((c.state_bits == 8) == S8 && (c.param_bf16 != 0) == PB && master == MA && (c.grad_bf16 != 0) == GB) \
-    bi::k_adamw<kMax, S8, PB, MA, GB><<<grid, bi::kAdamThreads, 0, s>>>(*tab, a);
-#define BI_ADAM_G(S8, PB, MA) BI_ADAM(S8, PB, MA, false) BI_ADAM(S8, PB, MA, true)
-#define BI_ADAM_P(S8) BI_ADAM_G(S8, false, false) BI_ADAM_G(S8, true, false) BI_ADAM_G(S8, true, true)
-  BI_ADAM_P(false)
-  BI_ADAM_P(true)
+  const int held = c.state_bits == 32 ? bi::kAdam32 : a.dither_m || a.dither_v ? bi::kAdam8Dither : bi::kAdam8;
+#define BI_ADAM(ST, PB, MA, GB)                                                                     \
+  if (held == ST && (c.param_bf16 != 0) == PB && master == MA && (c.grad_bf16 != 0) == GB) \
+    bi::k_adamw<kMax, ST, PB, MA, GB><<<grid, bi::kAdamThreads, 0, s>>>(*tab, a);
+#define BI_ADAM_G(ST, PB, MA) BI_ADAM(ST, PB, MA, false) BI_ADAM(ST, PB, MA, true)
+#define BI_ADAM_P(ST) BI_ADAM_G(ST, false, false) BI_ADAM_G(ST, true, false) BI_ADAM_G(ST, true, true)
+  BI_ADAM_P(bi::kAdam32)
+  BI_ADAM_P(bi::kAdam8)
+  BI_ADAM_P(bi::kAdam8Dither)
 #undef BI_ADAM_P
 #undef BI_ADAM_G
 #undef BI_ADAM
@@ -107,6 +109,9 @@ extern "C" bi_status bi_adamw_step(const bi_adamw_tensor* tensors, int32_t count
   a.lr = c.lr;
   a.beta1 = c.beta1;
   a.beta2 = c.beta2;
+  a.step = c.step;
+  a.dither_m = c.state_bits == 8 && c.beta1 > bi::kNearestBeta1;
+  a.dither_v = c.state_bits == 8 && c.beta2 > bi::kNearestBeta2;
   a.grad_scale = grad_scale;
   a.step_dev = step_dev;
   a.status = dev_status;

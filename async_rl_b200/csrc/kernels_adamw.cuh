@@ -25,6 +25,17 @@ constexpr float kE4m3Inv = 1.0f / 448.0f;
 constexpr float kF32Max = 3.4028235e38f;
 constexpr float kE4m3Tiny = 0.001953125f;           // 2^-9, the smallest positive value
 
+// Above these, states of 8 bits are not rounded to nearest.  A step moves m by 1 - beta1 and sqrt(v) by
+// (1 - beta2) / 2 of itself; where that is less than half a code's step (1/18 of 9/8) nearest gives the old code
+// back, and the state stands still.  beta1: the arithmetic bound.  beta2: the gradients' own scatter carries
+// sqrt(v) over the edge for a while.  Measured as held over true sqrt(v), 10% and 90% quantiles, some thousand
+// steps after 65,536 gradients changed their scales: nearest 0.91 and 1.10 (0.95), 0.90 and 1.11 (0.96), 0.90 and 1.20
+// (0.98), 0.92 and 4.8 (0.99), 0.44 and 4.7 (0.999); dithered 0.87 and 1.15, 0.86 and 1.16, 0.84 and 1.19,
+// 0.82 and 1.22, 0.79 and 1.26.  Dithering sqrt(v) costs 437 us for 357 of nearest (110 million elements; 447 and 480
+// with five and four blocks an SM), both states 470.
+constexpr double kNearestBeta1 = 17.0 / 18.0;
+constexpr double kNearestBeta2 = 0.96;
+
 struct AdamHyper {
   float b1, c1, b2, c2;   // beta1, 1 - beta1, beta2, 1 - beta2
   float rate, root, keep, eps;  // lr / (1 - beta1^t), 1 / sqrt(1 - beta2^t), 1 - lr wd, eps
@@ -47,6 +58,8 @@ struct AdamTable {
 struct AdamArgs {
   AdamHyper h;
   double lr, beta1, beta2;
+  int64_t step;
+  bool dither_m, dither_v;
   const float* grad_scale;
   const int64_t* step_dev;
   int32_t* status;
@@ -102,6 +115,26 @@ __device__ __forceinline__ uint32_t e4m3_down2(float lo, float hi) {
   return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
 }
 
+// 32 bits for element i of its tensor at step t: products with odd numbers from the fractions of irrational ones
+// (the golden ratio, roots of 11, 2, 17, 3 and 13), high bits folded onto low ones in between.
+__device__ __forceinline__ uint32_t adam_bits(int64_t i, int64_t t) {
+  uint32_t x = static_cast<uint32_t>(i) * 0x9E3779B9u + static_cast<uint32_t>(i >> 32) * 0x510E527Fu +
+               static_cast<uint32_t>(t) * 0x6A09E667u + static_cast<uint32_t>(t >> 32) * 0x1F83D9ABu;
+  x ^= x >> 16;
+  x *= 0xBB67AE85u;
+  x ^= x >> 15;
+  x *= 0x9B05688Du;
+  return x ^ (x >> 16);
+}
+// y as the e4m3 value below or above it in magnitude, above with the odds of its place between them, r in
+// [0, 65536).  |y| / spacing is below 16 and a power of two's multiple: exact; the sum is rounded.
+__device__ __forceinline__ float adam_dither(float y, uint32_t r) {
+  const uint32_t top = max(__float_as_uint(y) & 0x7f800000u, 0x3c800000u);  // 2^-6 and less: the spacing 2^-9
+  const float spacing = __uint_as_float(top - (3u << 23)), inv = __uint_as_float((257u << 23) - top);
+  const float c = floorf(__fadd_rn(__fmul_rn(fabsf(y), inv), __fmul_rn(static_cast<float>(r), 1.0f / 65536.0f)));
+  return copysignf(__fmul_rn(c, spacing), y);
+}
+
 // One element; every operation is rounded, none contracted, so a plain evaluation in the same order
 // gives the same bits (and with 8-bit states the same codes).
 __device__ __forceinline__ void adam_one(const AdamHyper& h, float gs, float g, float& p, float& m, float& v, float& root) {
@@ -119,9 +152,12 @@ __device__ __forceinline__ float adam_warp_max(float v) {
   return v;
 }
 
-// kState8: 8-bit states; kPBf16: bf16 params; kMaster: with fp32 masters; kGBf16: bf16 gradients
-template <int kMax, bool kState8, bool kPBf16, bool kMaster, bool kGBf16>
-__global__ void __launch_bounds__(kAdamThreads, kState8 ? 6 : 3) k_adamw(const __grid_constant__ AdamTable<kMax> tab, const AdamArgs a) {
+// kState: how states are held; kPBf16: bf16 params; kMaster: with fp32 masters; kGBf16: bf16 gradients
+enum AdamState : int { kAdam32 = 0, kAdam8 = 1, kAdam8Dither = 2 };
+template <int kMax, int kState, bool kPBf16, bool kMaster, bool kGBf16>
+__global__ void __launch_bounds__(kAdamThreads, kState == kAdam32 ? 3 : 6)
+    k_adamw(const __grid_constant__ AdamTable<kMax> tab, const AdamArgs a) {
+  constexpr bool kState8 = kState != kAdam32;
   __shared__ AdamHyper sh;
   AdamHyper h = a.h;
   if (a.step_dev) {
@@ -162,7 +198,8 @@ __global__ void __launch_bounds__(kAdamThreads, kState8 ? 6 : 3) k_adamw(const _
   const uint16_t* gb = static_cast<const uint16_t*>(t.g);
   // What a lane holds.  One unit a warp and, with 8-bit states, six blocks an SM: their step is bound by
   // the latency of its chain of conversions, roots and quotients, which warps hide better than loads ahead
-  // (110 million elements, bf16 gradients, masters: 342 us; two units with both loads ahead 413, four blocks 382).
+  // (110 million elements, bf16 gradients, masters: 342 us when it was chosen, two units with both loads ahead 413, four
+  // blocks 382; 357 now, and 413 with the step on the device, whose factors thread 0 of each block computes.)
   struct Held {
     F8 p, g, m, v;
     uint32_t mw[2], vw[2];
@@ -250,6 +287,11 @@ __global__ void __launch_bounds__(kAdamThreads, kState8 ? 6 : 3) k_adamw(const _
         const float r = __fmul_rn(root[e], iv);
         root[e] = root[e] > 0.f ? fmaxf(r, kE4m3Tiny) : r;
         x.m.x[e] = __fmul_rn(x.m.x[e], im);
+        if (kState == kAdam8Dither) {
+          const uint32_t bits = adam_bits(i0 + e, a.step_dev ? *a.step_dev : a.step);
+          if (a.dither_m) x.m.x[e] = adam_dither(x.m.x[e], bits & 0xffffu);
+          if (a.dither_v) root[e] = adam_dither(root[e], bits >> 16);
+        }
       }
 #pragma unroll
       for (int e = 0; e < 8; e += 2) {

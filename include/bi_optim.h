@@ -40,12 +40,17 @@ typedef struct bi_adamw_tensor {
 /*
  * 8-bit states: a block of 256 consecutive elements (the last one may be short) holds x as
  * code * scale with scale = max|x| * fl(1 / 448) (448 = the largest e4m3 value) and the code
- * x * (448 * fl(1 / max|x|)) rounded to nearest even; x is m for exp_avg and sqrt(v) for exp_avg_sq, whose
+ * y = x * (448 * fl(1 / max|x|)) rounded as below; x is m for exp_avg and sqrt(v) for exp_avg_sq, whose
  * root halves the range of exponents.  Where 448 * fl(1 / max|x|) is not finite (a maximum below 1.3e-36)
  * the block is held as zeros with scale 0.  A sqrt(v) above zero never becomes the code of zero (it takes the
  * smallest one, 2^-9): a zero there would turn a small gradient into an unbounded update.  max is taken of the
  * finite elements; one that is not finite is held as NaN, and the other elements of its block are what they would
  * be without it.
+ * Rounding: m to nearest even for beta1 <= 17/18, sqrt(v) for beta2 <= 0.96.  Above, nearest would give most
+ * elements their old code back at every step; y goes to the code below or above it in magnitude, spaced q, as
+ * q * floor(|y| / q + r / 65536) in fp32, so that the held value is right on average (sqrt(v) scatters by about 20%
+ * around it).  r is a number of 16 bits made of the element's index in its tensor and of t alone (kernels_adamw.cuh:
+ * adam_bits; the low half for m, the high half for sqrt(v)): the same call gives the same bits.
  */
 typedef struct bi_adamw_cfg {
   double lr, beta1, beta2, eps, weight_decay;
