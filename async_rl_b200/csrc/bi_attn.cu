@@ -10,7 +10,7 @@ namespace {
 using namespace bi::host;
 
 constexpr int kMaxSms = 160;
-constexpr size_t kPartBytesMax = size_t{128} << 20;  // partial rows of a split forward, at most
+constexpr size_t kPartBytesMax = size_t{128} << 20;  // partial rows of a split forward, at most (below 2^19 of them)
 
 struct Shape {
   int64_t Tq, Tk;
@@ -27,6 +27,11 @@ bool shape_ok(Shape& z) {
 }
 bool sizes_ok(const Shape& z) {
   return z.Tq >= 0 && z.Tk >= 0 && z.S >= 0 && z.Tq < (int64_t{1} << 31) - 512 && z.Tk < (int64_t{1} << 31) - 512;
+}
+// Units are counted in 32 bits: one for each sequence and tile at most, and the partial rows of a split forward.
+bool units_ok(const Shape& z) {
+  const int64_t most = (int64_t{1} << 31) - (int64_t{1} << 20);
+  return z.S + z.Tq / z.tpt < most && z.S + z.Tk / bi::kAtTile < most;
 }
 bool rows_ok(const void* p, int64_t ld, int32_t heads, int32_t D) {
   return p && aligned16(p) && ld >= static_cast<int64_t>(heads) * D && ld % 8 == 0;
@@ -196,7 +201,7 @@ void bi_debug_attn_wait_limit_once(uint64_t limit_ns) { g_wait_base_ns = limit_n
 
 size_t bi_attn_fwd_workspace_bytes(int64_t Tq, int64_t Tk, int32_t S, int32_t Hq, int32_t Hkv, int32_t D) {
   Shape z{Tq, Tk, S, Hq, Hkv, D, 0, 0};
-  if (!sizes_ok(z) || !shape_ok(z)) return 0;
+  if (!sizes_ok(z) || !shape_ok(z) || !units_ok(z)) return 0;
   return fwd_layout(z).total;
 }
 
@@ -207,6 +212,7 @@ bi_status bi_attn_fwd(const uint16_t* q, const uint16_t* k, const uint16_t* v, i
   Shape z{Tq, Tk, S, Hq, Hkv, D, 0, 0};
   if (!dev_status || !sizes_ok(z) || !(scale > 0.f) || !std::isfinite(scale)) return BI_ERR_INVALID_ARG;
   if (!shape_ok(z)) return BI_ERR_UNSUPPORTED_SHAPE;
+  if (!units_ok(z)) return BI_ERR_INVALID_ARG;
   if (S > 0 && (!q_offsets || !k_offsets)) return BI_ERR_INVALID_ARG;
   if (Tq > 0 && (!rows_ok(q, q_ld, Hq, D) || !out || !aligned16(out) || !lse))
     return BI_ERR_INVALID_ARG;
@@ -287,7 +293,7 @@ bi_status bi_attn_fwd(const uint16_t* q, const uint16_t* k, const uint16_t* v, i
 
 size_t bi_attn_bwd_workspace_bytes(int64_t Tq, int64_t Tk, int32_t S, int32_t Hq, int32_t Hkv, int32_t D) {
   Shape z{Tq, Tk, S, Hq, Hkv, D, 0, 0};
-  if (!sizes_ok(z) || !shape_ok(z)) return 0;
+  if (!sizes_ok(z) || !shape_ok(z) || !units_ok(z)) return 0;
   return bwd_layout(z).total;
 }
 
@@ -300,6 +306,7 @@ bi_status bi_attn_bwd(const uint16_t* dout, int64_t dout_ld, const uint16_t* q, 
   Shape z{Tq, Tk, S, Hq, Hkv, D, 0, 0};
   if (!dev_status || !sizes_ok(z) || !(scale > 0.f) || !std::isfinite(scale)) return BI_ERR_INVALID_ARG;
   if (!shape_ok(z)) return BI_ERR_UNSUPPORTED_SHAPE;
+  if (!units_ok(z)) return BI_ERR_INVALID_ARG;
   if (S > 0 && (!q_offsets || !k_offsets)) return BI_ERR_INVALID_ARG;
   if (Tq > 0 && (!rows_ok(q, q_ld, Hq, D) || !rows_ok(dout, dout_ld, Hq, D) || !rows_ok(dq, dq_ld, Hq, D) || !out ||
                  !aligned16(out) || !lse))

@@ -116,7 +116,7 @@ BI_API bi_status bi_qk_norm_rope_bwd(const uint16_t* dq_out, const uint16_t* dk_
  *   out [Tq][Hq][D] bf16, lse [Hq][Tq] float.  A query that sees no key gets zeros and -infinity.  Rows
  *     in no sequence are left as they were; key rows in none are not used, whatever they hold.
  *   scale > 0, finite;  D 64 or 128;  Hq a multiple of Hkv, Hq / Hkv <= 128, Hkv <= 4096;
- *   0 <= S;  0 <= Tq, Tk < 2^31 - 512
+ *   0 <= Tq, Tk < 2^31 - 512;  0 <= S, and S + Tq / floor(128 Hkv / Hq) and S + Tk / 128 below 2^31 - 2^20
  * A row's result has the same bits in any batch and whether it is computed among its sequence's other
  * queries (prefill) or alone over a cache (decode).  A NaN or infinity in a key or value row of a sequence
  * reaches every query of that sequence that shares a 128-row tile with one that sees it.
