@@ -23,10 +23,11 @@
 //
 // What bounds it.  A key tile takes a row tile 1024 clocks of products and, with every exponential on the
 // special function unit, as many of those.  Its scores, softmax, P and product follow one another, so two row
-// tiles take turns: one's products beside the other's softmax.  Measured: one causal 8K sequence, 32/8 heads
-// of 128: 477 us (1.15 PFLOP/s); 16K: 1.90 ms; 64 packed sequences of 256..2048, 12/2 heads: 421 us; decode
-// over 64 caches of up to 8K keys: 198 us (5.8 TB/s), where HBM is the bound.  Without any softmax, the 8K
-// case takes 358 us: the issuing thread and the barriers.
+// tiles take turns: one's products beside the other's softmax.  Measured, this kernel alone with pauses between
+// (calls back to back, with plan and joining and at the clock they settle at, in brackets): one causal 8K sequence,
+// 32/8 heads of 128: 475 us (1.16 PFLOP/s); 16K: 1.84 ms (2.14); 64 packed sequences of 256..2048, 12/2 heads:
+// 431 us (484); decode over 64 caches of up to 8K keys: 201 us (225), 5.7 TB/s, where HBM is the bound.  Without
+// any softmax, the 8K case takes 358 us: the issuing thread and the barriers.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -335,7 +336,9 @@ __device__ __forceinline__ float2 ex2_poly(float2 x) {
 // 2^x of a pair of columns.  The special function unit gives 16 results a clock and SM, as long for a
 // tile's scores as its products take, so some columns of every 16 go to the FMA units instead; which
 // ones is a matter of the column alone, so a row's bits do not depend on its batch.
-// (None, 2, 3 or 4 of 8 pairs: dK, dV and dQ of 16 sequences take 467, 463, 458 and 473 us together.)
+// None, 1, 2, 3 or 4 of 8 pairs, whole calls: forward of one 8K sequence, 32/8 heads of 128: 511, 501, 488, 499 and
+// 525 us, heads of 64: 440, 428, 433, 455 and 490; gradient: 1413, 1420, 1402, 1410 and 1442, heads of 64: 1146, 1129,
+// 1144, 1146 and 1185; gradient of 16 sequences of 1024..2048, 12/2 heads of 128: 447, 450, 441, 443 and 460.
 constexpr uint32_t kAtPoly = 0x94;  // pairs 2, 4 and 7 of 8
 __device__ __forceinline__ float2 at_ex2(int pair, float2 x) {
   if ((kAtPoly >> (pair % 8)) & 1) return ex2_poly(x);

@@ -15,8 +15,9 @@
 //
 // Both are bound by the tensor cores, with the exponentials (16 a clock and SM) next: 2048 and 1536
 // clocks of products (D = 128) against 1024 of exponentials a pair of tiles.  Measured: a pair of tiles takes
-// dK, dV 2700 clocks and dQ 1750; 64 packed causal sequences of 256..2048, 12/2 heads of 128: 632 and 539 us;
-// three of 4K..8K, 16/8 heads of 64: 670 and 476 us.
+// dK, dV 2700 clocks and dQ 1750; 64 packed causal sequences of 256..2048, 12/2 heads of 128: 591 and 514 us, with the
+// plan's 22 and the rows' numbers' 100 in front of them (a call among others takes 1409); three of 4K..8K, 16/8 heads of
+// 64: 676 and 474 us, 11 and 29 (1303).
 //
 // Rows behave as in the forward: a tile of 128 rows is floor(128 / G) tokens times the G heads that
 // share a key/value head, so the gradients of shared heads are added up in the accumulators.

@@ -14,9 +14,10 @@
 // or a few a lane, and shared through shared memory.  The angle is taken in turns in 64 bits
 // (position * inv_freq / 2 pi, whole turns dropped), because a far position times a frequency has
 // more than 24 significant bits; what is left, below half a turn, goes to sincospif in 32 bits.
-// Measured: 76,239 tokens of 14 heads of 128 take 126 us (4.3 TB/s), 131,072 of 40 heads backward 790 us
-// (5.1 TB/s).  The forward has 16 warps an SM with two slots of loads each in flight; three blocks an SM
-// instead of two spill registers (162 us).  Angles by a 64-bit fixed-point product measured the same.
+// Measured: 76,239 tokens of 14 heads of 128 take 124 us (4.4 TB/s), 131,072 of 40 heads backward 795 us
+// (5.1 TB/s).  The forward has 16 warps an SM (122 registers) with two slots of loads each in flight; three blocks an
+// SM instead of two spill registers (162 us).  The backward's sums of both gains fill its 128 registers, and 116 bytes a
+// thread spill.  Angles by a 64-bit fixed-point product measured the same.
 #pragma once
 
 #include <cuda_runtime.h>

@@ -96,8 +96,8 @@ class AdamWState:
     def _follow(self):
         """Tensors that are not what they were at the last step are checked again."""
         # All addresses and sizes in bytes, and what else a gradient is held to.  (57 parameters with masters and 32-bit
-        # states: 40 us of this call's 70; types and layouts of the states as well would be 20 more, and a state seen
-        # as another type or order of the same bytes is still the same memory.)
+        # states: a step takes 69 us, with the addresses alone 44.  Types and layouts of the states would be more
+        # still, and a state seen as another type or order of the same bytes is still the same memory.)
         params = self.params
         if (list(map(torch.Tensor.data_ptr, self._flat)) != self._ptrs or list(map(_nbytes, self._flat)) != self._nbytes or
                 list(map(_shape, params)) != self.shapes or list(map(_dtype, params)) != self._dtypes or
